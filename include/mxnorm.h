@@ -279,6 +279,115 @@ int mxfp8_gemm(const void* a_q, const void* a_s, const void* b_q, const void* b_
 int mxnorm_bwd_noalloc(const void* x, const void* dy, const void* gamma, const float* G,
                        void* dx, void* dgamma, int64_t T, int64_t D, void* stream);
 
+/* Type of every tensor of a layer-norm call (statistics are always fp32). */
+enum mxn_dtype { MXN_BF16 = 0, MXN_FP16 = 1, MXN_FP32 = 2 };
+
+/*
+ * Layer norm, the row normalisation that centres as well as scales; RMSNorm
+ * (above) is its form without the mean.  For every row of x, in fp32:
+ *   mean = sum(x) / D,  var = sum((x - mean)^2) / D,  rstd = 1 / sqrt(var + eps)
+ *   y = (x - mean) * rstd * gamma + beta               (one rounding to y's type)
+ * The squares are summed about the row's mean, so an offset far above the
+ * deviation costs no accuracy.  A row with a NaN or an infinity gives NaN.
+ * x       [T, ld_x] (first D columns used); any D from 1 to MXN_MAX_D, any
+ *         ld_x >= D.  Rows that start on 16-byte boundaries (D and ld_x
+ *         multiples of 16 bytes) move 16 bytes an access, others one element.
+ * gamma, beta  [D] or NULL (1 and 0).
+ * y       [T, D] dense (written); must not overlap x.
+ * mean, rstd   fp32 [T] (written) or NULL; the backward takes them.
+ * eps     >= 0, finite.
+ * dtype   enum mxn_dtype, of x, gamma, beta and y.
+ */
+int layernorm_fwd(const void* x, const void* gamma, const void* beta, void* y, float* mean, float* rstd,
+                  int64_t T, int64_t D, int64_t ld_x, float eps, int dtype, void* stream);
+
+/*
+ * Layer norm's backward.  With xh = (x - mean) * rstd and g = gamma * dy
+ * (gamma = 1 when NULL), per row:
+ *   dx     = rstd * (g - sum(g) / D - xh * sum(g * xh) / D)
+ *   dgamma = sum over rows of dy * xh,   dbeta = sum over rows of dy
+ * x [T, ld_x], dy [T, ld_dy], gamma [D] or NULL; mean, rstd fp32 [T] from
+ * layernorm_fwd.  dx [T, D] dense (written; must not overlap x or dy).
+ * dgamma, dbeta  [D] (written) or NULL, each for itself; fp32 sums in a fixed
+ *         order without atomics, rounded once.  T = 0 writes zeros.
+ * workspace  device scratch of at least layernorm_bwd_workspace_size(T, D,
+ *         dtype) bytes, 16-byte aligned; may be NULL when dgamma and dbeta
+ *         are.  Contents on entry are ignored.
+ * D up to 16384 (MXN_ERR_UNSUPPORTED beyond).
+ */
+int layernorm_bwd(const void* x, const void* dy, const void* gamma, const float* mean, const float* rstd, void* dx,
+                  void* dgamma, void* dbeta, int64_t T, int64_t D, int64_t ld_x, int64_t ld_dy, int dtype,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch bytes layernorm_bwd needs on the current device (0 if the arguments
+   are invalid). */
+size_t layernorm_bwd_workspace_size(int64_t T, int64_t D, int dtype);
+
+/* Activation of the gate. */
+enum mxn_act {
+    MXN_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+    MXN_ACT_GELU = 1,      /* g * Phi(g), Phi the normal distribution function */
+    MXN_ACT_GELU_TANH = 2  /* g * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))) / 2 */
+};
+
+/*
+ * Gated feed-forward projection in bf16 on the tcgen05 tensor cores, the
+ * consumer of the normalised row in the feed-forward half of a block: both
+ * projections, the activation and the product in one kernel.
+ *   gate = x w_gate^T,  up = x w_up^T,  h = act(gate) * up
+ * accumulated in fp32; h is rounded once, from the fp32 gate and up.
+ * x       bf16 [T, ld_x], D columns used
+ * w_gate, w_up  bf16 [F, ld_w], D columns used: one output feature per row
+ * h       bf16 [T, F] (written)
+ * gate, up      bf16 [T, F] (written), or both NULL; the backward takes them.
+ * D, F, ld_x and ld_w are multiples of 8, ld >= D; any T (one token included).
+ * Outputs must not overlap inputs.
+ */
+int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up, int64_t T,
+                  int64_t D, int64_t F, int64_t ld_x, int64_t ld_w, int act, void* stream);
+
+/*
+ * Its backward, from dh [T, F] and the gate and up that gated_ffn_fwd kept:
+ *   dg = dh * up * act'(gate),  du = dh * act(gate)       (bf16, in the workspace)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * dh, gate, up bf16 [T, F] dense; x, w_gate, w_up, D, F, ld as in gated_ffn_fwd.
+ * dx      bf16 [T, D] (written) or NULL
+ * dw_gate, dw_up  bf16 [F, D] (written), or both NULL.  T = 0 writes zeros.
+ * Sums are fp32 in tensor memory, in a fixed order: no atomics.
+ * workspace  device scratch of at least gated_ffn_bwd_workspace_size(T, F)
+ *         bytes, 16-byte aligned.  Contents on entry are ignored.
+ */
+int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
+                  const void* up, void* dx, void* dw_gate, void* dw_up, int64_t T, int64_t D, int64_t F, int64_t ld_x,
+                  int64_t ld_w, int act, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch bytes gated_ffn_bwd needs: dg and du (0 if the arguments are invalid). */
+size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t F);
+
+/* Output of mxfp8_gated_ffn. */
+enum mxn_ffn_out {
+    MXN_FFN_BF16 = 0,  /* h bf16 [T, F] */
+    /* h quantised as by mxfp8_cast with nearest-even rounding, straight from
+       the fp32 product: E4M3 codes uint8 [T, F] and E8M0 scales. */
+    MXN_FFN_MXFP8 = 1
+};
+
+/*
+ * Gated feed-forward projection on MXFP8 operands (tcgen05 block-scaled MMA):
+ * h = act(A w_gate^T) * (A w_up^T) with A [T, K] and w_gate, w_up [F, K] as in
+ * mxfp8_gemm -- E4M3 codes, K contiguous, and scales in the MXN_SCALES_MMA
+ * layout (mxnorm_scales_bytes bytes each; padding bytes may hold anything).
+ * With MXN_FFN_MXFP8 the result is the A operand of the next mxfp8_gemm.
+ * h       bf16 [T, F], or uint8 [T, F] E4M3 codes (written)
+ * h_s     uint8, mxnorm_scales_bytes(T, F, scale_layout) bytes (written; in
+ *         the MMA layout padding bytes are not), for MXN_FFN_MXFP8; else NULL
+ * K a multiple of 128 (MXN_ERR_UNSUPPORTED otherwise); F a multiple of 8, of
+ * 32 for MXN_FFN_MXFP8; any T (one token included).
+ */
+int mxfp8_gated_ffn(const void* a_q, const void* a_s, const void* g_q, const void* g_s, const void* u_q,
+                    const void* u_s, void* h, void* h_s, int64_t T, int64_t F, int64_t K, int act, int out,
+                    int scale_layout, void* stream);
+
 /* Message for the last error on the calling thread ("" if none).  The string
    stays valid until the thread's next call into the library. */
 const char* mxnorm_last_error(void);

@@ -9,7 +9,10 @@
 #include <tuple>
 
 #include "fwd_dispatch.h"
+#include "gated_ffn.h"
+#include "gated_mxfp8.h"
 #include "gemm_mxfp8.h"
+#include "layernorm.h"
 #include "mxnorm.h"
 #include "row_bwd.cuh"
 #include "row_fwd.cuh"
@@ -762,6 +765,203 @@ int mxfp8_gemm(const void* a_q, const void* a_s, const void* b_q, const void* b_
   const int e = gemm_mxfp8_launch(a_q, a_s, b_q, b_s, c, (int)M, (int)N, (int)K, dev.sms, dev.status,
                                   static_cast<cudaStream_t>(stream), &why);
   if (e) return fail(MXN_ERR_CUDA, "mxfp8_gemm: %s", why);
+  return MXN_OK;
+}
+
+// Shape checks of the layer-norm entry points (any D and row stride).
+static int check_ln(const void* x, const char* name, int64_t T, int64_t D, int64_t ld, int64_t max_d, int dtype) {
+  t_empty = (T == 0);
+  if (T < 0) return fail(MXN_ERR_ARG, "T = %lld < 0", (long long)T);
+  if (D <= 0) return fail(MXN_ERR_ARG, "D = %lld is not positive", (long long)D);
+  if (D > max_d) return fail(MXN_ERR_UNSUPPORTED, "D = %lld > %lld", (long long)D, (long long)max_d);
+  if (ld < D) return fail(MXN_ERR_ARG, "row stride of %s, %lld, is below D", name, (long long)ld);
+  if (dtype < MXN_BF16 || dtype > MXN_FP32) return fail(MXN_ERR_ARG, "dtype = %d", dtype);
+  return check_out(x, name);
+}
+
+int layernorm_fwd(const void* x, const void* gamma, const void* beta, void* y, float* mean, float* rstd, int64_t T,
+                  int64_t D, int64_t ld_x, float eps, int dtype, void* stream) {
+  t_err.clear();
+  int rc = check_ln(x, "x", T, D, ld_x, MXN_MAX_D, dtype);
+  if (!rc) rc = check_out(y, "y");
+  if (!rc) rc = check_opt(gamma, "gamma");
+  if (!rc) rc = check_opt(beta, "beta");
+  if (!rc) rc = check_opt(mean, "mean");
+  if (!rc) rc = check_opt(rstd, "rstd");
+  if (rc) return rc;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(MXN_ERR_ARG, "eps = %g", (double)eps);
+  if ((rc = injected())) return rc;
+  if (T == 0) return MXN_OK;
+  DeviceInfo dev;
+  if ((rc = device_info(&dev))) return rc;
+  const char* why = "";
+  const int e = layernorm_fwd_launch(x, gamma, beta, y, mean, rstd, T, (int)D, ld_x, eps, dtype, dev.sms,
+                                     static_cast<cudaStream_t>(stream), &why);
+  if (e) return cuda_fail((cudaError_t)e, why);
+  return MXN_OK;
+}
+
+size_t layernorm_bwd_workspace_size(int64_t T, int64_t D, int dtype) {
+  if (T <= 0 || D <= 0 || D > kLnMaxBwdD || dtype < MXN_BF16 || dtype > MXN_FP32) return 0;
+  DeviceInfo dev;
+  if (device_info(&dev)) return 0;
+  return layernorm_bwd_workspace(T, (int)D, dtype, dev.sms);
+}
+
+int layernorm_bwd(const void* x, const void* dy, const void* gamma, const float* mean, const float* rstd, void* dx,
+                  void* dgamma, void* dbeta, int64_t T, int64_t D, int64_t ld_x, int64_t ld_dy, int dtype,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  t_err.clear();
+  int rc = check_ln(x, "x", T, D, ld_x, kLnMaxBwdD, dtype);
+  if (!rc) rc = check_ln(dy, "dy", T, D, ld_dy, kLnMaxBwdD, dtype);
+  if (!rc) rc = check_out(mean, "mean");
+  if (!rc) rc = check_out(rstd, "rstd");
+  if (!rc) rc = check_out(dx, "dx");
+  if (!rc) rc = check_opt(gamma, "gamma");
+  if (!rc) rc = check_opt(dgamma, "dgamma");
+  if (!rc) rc = check_opt(dbeta, "dbeta");
+  if (rc) return rc;
+  if (dgamma && !gamma) return fail(MXN_ERR_ARG, "dgamma requested without gamma");
+  if ((rc = injected())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const size_t bytes = (size_t)D * (dtype == MXN_FP32 ? 4 : 2);
+    for (void* p : {dgamma, dbeta})
+      if (p) {
+        const cudaError_t e = cudaMemsetAsync(p, 0, bytes, s);
+        if (e != cudaSuccess) return cuda_fail(e, "layernorm_bwd: cudaMemsetAsync");
+      }
+    return MXN_OK;
+  }
+  DeviceInfo dev;
+  if ((rc = device_info(&dev))) return rc;
+  if (dgamma || dbeta) {
+    const size_t need = layernorm_bwd_workspace(T, (int)D, dtype, dev.sms);
+    if (!workspace || !aligned16(workspace))
+      return fail(MXN_ERR_ARG, "workspace is NULL or not 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(MXN_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  }
+  const char* why = "";
+  const int e = layernorm_bwd_launch(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, T, (int)D, ld_x, ld_dy, dtype,
+                                     workspace, dev.sms, dev.status, s, &why);
+  if (e) return cuda_fail((cudaError_t)e, why);
+  return MXN_OK;
+}
+
+// Largest row count, width and row stride of the feed-forward entry points.
+static constexpr int64_t kFfnMax = 1 << 30;
+
+static int check_ffn(int64_t T, int64_t D, int64_t F, int64_t ld_x, int64_t ld_w, int act) {
+  t_empty = (T == 0);
+  if (T < 0) return fail(MXN_ERR_ARG, "T = %lld < 0", (long long)T);
+  if (D <= 0 || D % 8) return fail(MXN_ERR_ARG, "D = %lld is not a positive multiple of 8", (long long)D);
+  if (F <= 0 || F % 8) return fail(MXN_ERR_ARG, "F = %lld is not a positive multiple of 8", (long long)F);
+  if (ld_x < D || ld_x % 8) return fail(MXN_ERR_ARG, "ld_x = %lld must be >= D and a multiple of 8", (long long)ld_x);
+  if (ld_w < D || ld_w % 8) return fail(MXN_ERR_ARG, "ld_w = %lld must be >= D and a multiple of 8", (long long)ld_w);
+  if (act < MXN_ACT_SILU || act > MXN_ACT_GELU_TANH) return fail(MXN_ERR_ARG, "act = %d", act);
+  if (T > kFfnMax || D > kFfnMax || F > kFfnMax || ld_x > kFfnMax || ld_w > kFfnMax)
+    return fail(MXN_ERR_UNSUPPORTED, "shape too large");
+  return MXN_OK;
+}
+
+int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up, int64_t T,
+                  int64_t D, int64_t F, int64_t ld_x, int64_t ld_w, int act, void* stream) {
+  t_err.clear();
+  int rc = check_ffn(T, D, F, ld_x, ld_w, act);
+  if (!rc) rc = check_out(x, "x");
+  if (!rc) rc = check_out(w_gate, "w_gate");
+  if (!rc) rc = check_out(w_up, "w_up");
+  if (!rc) rc = check_out(h, "h");
+  if (!rc) rc = check_opt(gate, "gate");
+  if (!rc) rc = check_opt(up, "up");
+  if (rc) return rc;
+  if (!t_empty && !gate != !up) return fail(MXN_ERR_ARG, "gate and up are kept together");
+  if ((rc = injected())) return rc;
+  if (T == 0) return MXN_OK;
+  DeviceInfo dev;
+  if ((rc = device_info(&dev))) return rc;
+  const char* why = "";
+  const int e = gated_ffn_fwd_launch(x, w_gate, w_up, h, gate, up, (int)T, (int)D, (int)F, ld_x, ld_w, act, dev.sms,
+                                     dev.status, static_cast<cudaStream_t>(stream), &why);
+  if (e) return fail(MXN_ERR_CUDA, "gated_ffn_fwd: %s", why);
+  return MXN_OK;
+}
+
+size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t F) {
+  if (T <= 0 || F <= 0 || F % 8 || T > kFfnMax || F > kFfnMax) return 0;
+  return (size_t)2 * sizeof(uint16_t) * (size_t)T * (size_t)F;
+}
+
+int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
+                  const void* up, void* dx, void* dw_gate, void* dw_up, int64_t T, int64_t D, int64_t F, int64_t ld_x,
+                  int64_t ld_w, int act, void* workspace, size_t workspace_bytes, void* stream) {
+  t_err.clear();
+  int rc = check_ffn(T, D, F, ld_x, ld_w, act);
+  const void* in[6] = {dh, x, w_gate, w_up, gate, up};
+  const char* names[6] = {"dh", "x", "w_gate", "w_up", "gate", "up"};
+  for (int i = 0; i < 6 && !rc; ++i) rc = check_out(in[i], names[i]);
+  if (!rc) rc = check_opt(dx, "dx");
+  if (!rc) rc = check_opt(dw_gate, "dw_gate");
+  if (!rc) rc = check_opt(dw_up, "dw_up");
+  if (rc) return rc;
+  if (!dw_gate != !dw_up) return fail(MXN_ERR_ARG, "dw_gate and dw_up are written together");
+  if ((rc = injected())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    for (void* p : {dw_gate, dw_up})
+      if (p) {
+        const cudaError_t e = cudaMemsetAsync(p, 0, (size_t)F * (size_t)D * sizeof(uint16_t), s);
+        if (e != cudaSuccess) return cuda_fail(e, "gated_ffn_bwd: cudaMemsetAsync");
+      }
+    return MXN_OK;
+  }
+  if (!dx && !dw_gate) return MXN_OK;
+  const size_t need = gated_ffn_bwd_workspace_size(T, F);
+  if (!workspace || !aligned16(workspace)) return fail(MXN_ERR_ARG, "workspace is NULL or not 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(MXN_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  DeviceInfo dev;
+  if ((rc = device_info(&dev))) return rc;
+  uint16_t* dg = static_cast<uint16_t*>(workspace);
+  const char* why = "";
+  const int e = gated_ffn_bwd_launch(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, dg, dg + T * F, (int)T,
+                                     (int)D, (int)F, ld_x, ld_w, act, dev.sms, dev.status, s, &why);
+  if (e) return fail(MXN_ERR_CUDA, "gated_ffn_bwd: %s", why);
+  return MXN_OK;
+}
+
+int mxfp8_gated_ffn(const void* a_q, const void* a_s, const void* g_q, const void* g_s, const void* u_q,
+                    const void* u_s, void* h, void* h_s, int64_t T, int64_t F, int64_t K, int act, int out,
+                    int scale_layout, void* stream) {
+  t_err.clear();
+  t_empty = (T == 0);
+  if (T < 0) return fail(MXN_ERR_ARG, "T = %lld < 0", (long long)T);
+  if (out != MXN_FFN_BF16 && out != MXN_FFN_MXFP8) return fail(MXN_ERR_ARG, "out = %d", out);
+  if (scale_layout != MXN_SCALES_ROWMAJOR && scale_layout != MXN_SCALES_MMA)
+    return fail(MXN_ERR_ARG, "scale_layout = %d", scale_layout);
+  if (act < MXN_ACT_SILU || act > MXN_ACT_GELU_TANH) return fail(MXN_ERR_ARG, "act = %d", act);
+  const int unit = out == MXN_FFN_MXFP8 ? 32 : 8;
+  if (F <= 0 || F % unit) return fail(MXN_ERR_ARG, "F = %lld is not a positive multiple of %d", (long long)F, unit);
+  if (K <= 0) return fail(MXN_ERR_ARG, "K = %lld is not positive", (long long)K);
+  if (K % 128) return fail(MXN_ERR_UNSUPPORTED, "mxfp8_gated_ffn: K %% 128 must be 0 (K = %lld)", (long long)K);
+  if (T > kFfnMax || F > kFfnMax || K > kFfnMax) return fail(MXN_ERR_UNSUPPORTED, "shape too large");
+  const void* ptrs[7] = {a_q, a_s, g_q, g_s, u_q, u_s, h};
+  const char* names[7] = {"a_q", "a_s", "g_q", "g_s", "u_q", "u_s", "h"};
+  int rc = MXN_OK;
+  for (int i = 0; i < 7 && !rc; ++i) rc = check_out(ptrs[i], names[i]);
+  if (!rc && out == MXN_FFN_MXFP8) rc = check_out(h_s, "h_s");
+  if (rc) return rc;
+  if (out == MXN_FFN_BF16 && h_s) return fail(MXN_ERR_ARG, "h_s is given for bf16 output");
+  if ((rc = injected())) return rc;
+  if (T == 0) return MXN_OK;
+  DeviceInfo dev;
+  if ((rc = device_info(&dev))) return rc;
+  const char* why = "";
+  const int e = gated_mxfp8_launch(a_q, a_s, g_q, g_s, u_q, u_s, h, h_s, (int)T, (int)F, (int)K, act,
+                                   scale_layout == MXN_SCALES_MMA, dev.sms, dev.status,
+                                   static_cast<cudaStream_t>(stream), &why);
+  if (e) return fail(MXN_ERR_CUDA, "mxfp8_gated_ffn: %s", why);
   return MXN_OK;
 }
 

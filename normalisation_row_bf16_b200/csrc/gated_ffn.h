@@ -1,0 +1,24 @@
+// gated_ffn.h -- launchers of the bf16 gated feed-forward kernels (gated_ffn.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mxn {
+
+enum { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2 };
+
+// Arguments are checked by the caller: T >= 1; D, F, ld_x, ld_w multiples of 8;
+// pointers 16-byte aligned; sizes below 2^31.  Return 0, or non-zero with *why set.
+int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up, int T,
+                         int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
+                         cudaStream_t stream, const char** why);
+
+// dg, du: bf16 [T, F] scratch.  dx, and the pair dw_gate, dw_up, may be null.
+int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
+                         const void* up, void* dx, void* dw_gate, void* dw_up, void* dg, void* du, int T, int D,
+                         int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
+                         const char** why);
+
+}  // namespace mxn

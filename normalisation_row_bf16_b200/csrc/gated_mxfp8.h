@@ -1,0 +1,17 @@
+// gated_mxfp8.h -- launcher of the MXFP8 gated feed-forward kernel (gated_mxfp8.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mxn {
+
+// Arguments are checked by the caller: T >= 1; K % 128 == 0; F a multiple of 8
+// (bf16 output) or 32 (E4M3 output); pointers 16-byte aligned; sizes below
+// 2^31.  h_s is null for bf16 output.  scale_mma: layout of h_s.
+// Returns 0, or non-zero with *why set.
+int gated_mxfp8_launch(const void* a_q, const void* a_s, const void* g_q, const void* g_s, const void* u_q,
+                       const void* u_s, void* h, void* h_s, int T, int F, int K, int act, bool scale_mma, int sms,
+                       unsigned* status, cudaStream_t stream, const char** why);
+
+}  // namespace mxn

@@ -7,6 +7,7 @@ tensors, raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -19,6 +20,9 @@ RNE, SR = 0, 1
 SCALES_ROWMAJOR, SCALES_MMA = 0, 1
 ELEM = {"e4m3": 0, "e2m1": 1, "nvfp4": 2}
 STAT = {"absmax": 0, "scale_exp": 1}
+DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+FFN_OUT = {"bf16": 0, "e4m3": 1}
 MXN_OK, MXN_ERR_ARG, MXN_ERR_UNSUPPORTED, MXN_ERR_CUDA, MXN_ERR_TIMEOUT = 0, -1, -2, -3, -4
 
 # Every symbol include/mxnorm.h declares, with its ctypes signature.
@@ -39,6 +43,13 @@ SIGNATURES = {
     "mxnorm_bwd_workspace_size": (_SZ, [_I64, _I64]),
     "mxnorm_bwd_noalloc": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _P]),
     "mxfp8_gemm": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "layernorm_fwd": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _I32, _P]),
+    "layernorm_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _SZ, _P]),
+    "layernorm_bwd_workspace_size": (_SZ, [_I64, _I64, _I32]),
+    "gated_ffn_fwd": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P]),
+    "gated_ffn_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P, _SZ, _P]),
+    "gated_ffn_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "mxfp8_gated_ffn": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P]),
     "mxnorm_last_error": (ctypes.c_char_p, []),
     "mxnorm_device_status": (_I32, [_P]),
     "mxnorm_set_tuning": (_I32, [_I32, _I32, _I32]),
@@ -294,6 +305,201 @@ def mxfp8_gemm(a_q, a_s, b_q, b_s, M: int, N: int, K: int, c=None, stream=None):
     return c
 
 
+def _input(t, name, shape, dtype, device, dense: bool = True):
+    """An input tensor of the given shape and type on `device`, its rows (last
+    dimension) contiguous; dense: the whole tensor is."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not (t.is_contiguous() if dense else t.numel() == 0 or t.stride(-1) == 1 or t.shape[-1] == 1):
+        raise ValueError(f"{name} must be contiguous" if dense else f"rows of {name} must be contiguous")
+    return t
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (its width where it has at most one row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _current(x):
+    """The library launches on the current device: refuse tensors of another."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return x.device
+
+
+def _on(stream):
+    """Context in which outputs and workspaces are allocated: memory of the
+    stream the kernels run on, so that the allocator orders its reuse."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _output(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_buffer(t, name, math.prod(shape) * dtype.itemsize, dtype, device)
+    return t
+
+
+def layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
+                  want_stats: bool = True, stream=None):
+    """Layer norm over the rows of x [T, D] (bf16, fp16 or fp32; any D and row
+    stride): returns (y [T, D], mean fp32 [T], rstd fp32 [T]); the statistics
+    are None with want_stats=False, unless buffers are given."""
+    dev = _current(x)
+    if x.dim() != 2 or x.dtype not in DTYPE:
+        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
+    T, D = x.shape
+    _input(x, "x", (T, D), x.dtype, dev, dense=False)
+    if gamma is not None:
+        _input(gamma, "gamma", (D,), x.dtype, dev)
+    if beta is not None:
+        _input(beta, "beta", (D,), x.dtype, dev)
+    with _on(stream):
+        y = _output(y, "y", (T, D), x.dtype, dev)
+        if want_stats or mean is not None:
+            mean = _output(mean, "mean", (T,), torch.float32, dev)
+        if want_stats or rstd is not None:
+            rstd = _output(rstd, "rstd", (T,), torch.float32, dev)
+    _check(lib().layernorm_fwd(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd), T, D, _ld(x),
+                               float(eps), DTYPE[x.dtype], _stream(stream)))
+    return y, mean, rstd
+
+
+def layernorm_bwd(x, dy, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, workspace=None,
+                  want_dgamma: bool = True, want_dbeta: bool = True, stream=None):
+    """Layer norm's backward: returns (dx [T, D], dgamma [D] or None, dbeta [D]
+    or None).  gamma may be None; there is then no dgamma."""
+    dev = _current(x)
+    if x.dim() != 2 or x.dtype not in DTYPE:
+        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
+    T, D = x.shape
+    _input(x, "x", (T, D), x.dtype, dev, dense=False)
+    _input(dy, "dy", (T, D), x.dtype, dev, dense=False)
+    if gamma is not None:
+        _input(gamma, "gamma", (D,), x.dtype, dev)
+    _input(mean, "mean", (T,), torch.float32, dev)
+    _input(rstd, "rstd", (T,), torch.float32, dev)
+    nbytes = 0
+    with _on(stream):
+        dx = _output(dx, "dx", (T, D), x.dtype, dev)
+        if dgamma is not None or (want_dgamma and gamma is not None):
+            dgamma = _output(dgamma, "dgamma", (D,), x.dtype, dev)
+        if dbeta is not None or want_dbeta:
+            dbeta = _output(dbeta, "dbeta", (D,), x.dtype, dev)
+        if dgamma is not None or dbeta is not None:
+            nbytes = int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[x.dtype]))
+            workspace = _workspace(workspace, nbytes, dev)
+            nbytes = workspace.numel() * workspace.element_size()
+    _check(lib().layernorm_bwd(_ptr(x), _ptr(dy), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dgamma),
+                               _ptr(dbeta), T, D, _ld(x), _ld(dy), DTYPE[x.dtype], _ptr(workspace), nbytes,
+                               _stream(stream)))
+    return dx, dgamma, dbeta
+
+
+def layernorm_bwd_workspace_bytes(T: int, D: int, dtype=torch.bfloat16) -> int:
+    return int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[dtype]))
+
+
+def _workspace(t, nbytes, device):
+    if t is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    _check_buffer(t, "workspace", nbytes, t.dtype, device)
+    return t
+
+
+def _ffn_inputs(x, w_gate, w_up, act):
+    dev = _current(x)
+    if act not in ACT:
+        raise ValueError(f"unknown activation {act!r}")
+    if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("x must be [T, D] and the weights [F, D]")
+    T, D, F = x.shape[0], x.shape[1], w_gate.shape[0]
+    _input(x, "x", (T, D), torch.bfloat16, dev, dense=False)
+    _input(w_gate, "w_gate", (F, D), torch.bfloat16, dev, dense=False)
+    _input(w_up, "w_up", (F, D), torch.bfloat16, dev, dense=False)
+    if _ld(w_gate) != _ld(w_up):
+        raise ValueError("w_gate and w_up must have the same row stride")
+    return dev, T, D, F
+
+
+def gated_ffn_fwd(x, w_gate, w_up, act: str = "silu", save: bool = False, h=None, gate=None, up=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T) in bf16: returns (h [T, F], gate, up).
+    save: keep the projections [T, F] for gated_ffn_bwd (else None); act:
+    "silu", "gelu" or "gelu_tanh"."""
+    dev, T, D, F = _ffn_inputs(x, w_gate, w_up, act)
+    with _on(stream):
+        h = _output(h, "h", (T, F), torch.bfloat16, dev)
+        if save or gate is not None or up is not None:
+            gate = _output(gate, "gate", (T, F), torch.bfloat16, dev)
+            up = _output(up, "up", (T, F), torch.bfloat16, dev)
+    _check(lib().gated_ffn_fwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(gate), _ptr(up), T, D, F, _ld(x),
+                               _ld(w_gate), ACT[act], _stream(stream)))
+    return h, gate, up
+
+
+def gated_ffn_bwd_workspace_bytes(T: int, F: int) -> int:
+    return int(lib().gated_ffn_bwd_workspace_size(T, F))
+
+
+def gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None, dw_gate=None, dw_up=None,
+                  workspace=None, want_dx: bool = True, want_dw: bool = True, stream=None):
+    """Backward of gated_ffn_fwd from the gate and up it kept: returns
+    (dx [T, D], dw_gate [F, D], dw_up [F, D]), None where not wanted."""
+    dev, T, D, F = _ffn_inputs(x, w_gate, w_up, act)
+    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
+        _input(t, name, (T, F), torch.bfloat16, dev)
+    with _on(stream):
+        if want_dx or dx is not None:
+            dx = _output(dx, "dx", (T, D), torch.bfloat16, dev)
+        if want_dw or dw_gate is not None or dw_up is not None:
+            dw_gate = _output(dw_gate, "dw_gate", (F, D), torch.bfloat16, dev)
+            dw_up = _output(dw_up, "dw_up", (F, D), torch.bfloat16, dev)
+        workspace = _workspace(workspace, 4 * T * F, dev)
+    _check(lib().gated_ffn_bwd(_ptr(dh), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dx),
+                               _ptr(dw_gate), _ptr(dw_up), T, D, F, _ld(x), _ld(w_gate), ACT[act], _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dx, dw_gate, dw_up
+
+
+def mxfp8_gated_ffn(a_q, a_s, g_q, g_s, u_q, u_s, T: int, F: int, K: int, act: str = "silu", out: str = "bf16",
+                    scale_layout: int = SCALES_MMA, h=None, h_s=None, stream=None):
+    """h = act(A Wg^T) * (A Wu^T) on MXFP8 operands (codes, and scales in the
+    MMA layout): returns (h bf16 [T, F], None), or with out="e4m3" (codes
+    uint8 [T, F], scales uint8), the A operand of the next mxfp8_gemm."""
+    dev = _current(a_q)
+    if act not in ACT or out not in FFN_OUT:
+        raise ValueError(f"unknown activation {act!r} or output {out!r}")
+    for t, name, rows in ((a_q, "a_q", T), (g_q, "g_q", F), (u_q, "u_q", F)):
+        _check_buffer(t, name, rows * K, torch.uint8, dev)
+    for t, name, rows in ((a_s, "a_s", T), (g_s, "g_s", F), (u_s, "u_s", F)):
+        _check_buffer(t, name, scales_bytes(rows, K, SCALES_MMA), torch.uint8, dev)
+        if t is None:
+            raise ValueError(f"{name} is missing")
+    with _on(stream):
+        if out == "bf16":
+            h = _output(h, "h", (T, F), torch.bfloat16, dev)
+            if h_s is not None:
+                raise ValueError("h_s is given for bf16 output")
+        else:
+            h = _output(h, "h", (T, F), torch.uint8, dev)
+            n = scales_bytes(T, F, scale_layout)
+            _check_buffer(h_s, "h_s", n, torch.uint8, dev)
+            if h_s is None:
+                h_s = (torch.empty(T, F // 32, dtype=torch.uint8, device=dev) if scale_layout == SCALES_ROWMAJOR
+                       else torch.zeros(max(n, 1), dtype=torch.uint8, device=dev))
+    _check(lib().mxfp8_gated_ffn(_ptr(a_q), _ptr(a_s), _ptr(g_q), _ptr(g_s), _ptr(u_q), _ptr(u_s), _ptr(h),
+                                 _ptr(h_s), T, F, K, ACT[act], FFN_OUT[out], int(scale_layout), _stream(stream)))
+    return h, h_s
+
+
 def device_status(stream=None) -> int:
     """Synchronises the stream and returns (and clears) the device status."""
     return int(lib().mxnorm_device_status(_stream(stream)))
@@ -319,4 +525,4 @@ def algorithmic_bytes_fwd(T: int, D: int, gamma: bool = True, G_out: bool = True
     return T * D * 2 + T * D + T * (D // 32) + (2 * D if gamma else 0) + (4 * T if G_out else 0)
 
 
-__all__ = [n for n in dir() if not n.startswith("_") and n not in ("ctypes", "math", "os", "torch")]
+__all__ = [n for n in dir() if not n.startswith("_") and n not in ("contextlib", "ctypes", "math", "os", "torch")]
