@@ -305,47 +305,73 @@ def mxfp8_gemm(a_q, a_s, b_q, b_s, M: int, N: int, K: int, c=None, stream=None):
     return c
 
 
-def _input(t, name, shape, dtype, device, dense: bool = True):
-    """An input tensor of the given shape and type on `device`, its rows (last
-    dimension) contiguous; dense: the whole tensor is."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype or tuple(t.shape) != shape:
+# The host's share of a small call counts as much as the kernel's: checks below
+# read each property once, and the default stream is asked for as a raw handle.
+
+def _input(t, name, shape, dtype, dev, dense: bool = True):
+    """Checks an input tensor: shape, type, CUDA device index; rows (the last
+    dimension) contiguous, with `dense` the whole tensor.  Its data pointer."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not (t.is_contiguous() if dense else t.numel() == 0 or t.stride(-1) == 1 or t.shape[-1] == 1):
-        raise ValueError(f"{name} must be contiguous" if dense else f"rows of {name} must be contiguous")
-    return t
+    if not t.is_contiguous():
+        if dense:
+            raise ValueError(f"{name} must be contiguous")
+        if t.stride(-1) != 1 and shape[-1] != 1:
+            raise ValueError(f"rows of {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _ld(t):
     """Row stride of a 2-D tensor (its width where it has at most one row)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else cols
 
 
 def _current(x):
-    """The library launches on the current device: refuse tensors of another."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+    """x's device index; the library launches on the current device, so
+    tensors of another one are refused."""
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return x.device
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _on(stream):
-    """Context in which outputs and workspaces are allocated: memory of the
-    stream the kernels run on, so that the allocator orders its reuse."""
-    if stream is None:
-        return contextlib.nullcontext()
+@contextlib.contextmanager
+def _on(stream, dev):
+    """The raw handle of the stream to launch on.  Outputs and workspaces are
+    allocated inside: memory of that stream, so that the allocator orders its
+    reuse after the kernels."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
 
 
-def _output(t, name, shape, dtype, device):
+def _output(t, name, shape, dtype, like):
+    """A new tensor, or the caller's buffer checked against what will be written."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check_buffer(t, name, math.prod(shape) * dtype.itemsize, dtype, device)
+        return like.new_empty(shape, dtype=dtype)
+    _check_buffer(t, name, math.prod(shape) * dtype.itemsize, dtype, like.device)
     return t
+
+
+def _workspace(t, nbytes, like):
+    if t is None:
+        return like.new_empty(max(nbytes, 16), dtype=torch.uint8)
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("workspace must be a tensor")
+    _check_buffer(t, "workspace", nbytes, t.dtype, like.device)
+    return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
@@ -354,23 +380,32 @@ def layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, y=None, mean=None
     stride): returns (y [T, D], mean fp32 [T], rstd fp32 [T]); the statistics
     are None with want_stats=False, unless buffers are given."""
     dev = _current(x)
-    if x.dim() != 2 or x.dtype not in DTYPE:
+    if stream is not None:
+        with _on(stream, dev) as s:
+            return _layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, dev, s)
+    return _layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, dev, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, dev, stream):
+    dtype = x.dtype
+    if x.dim() != 2 or dtype not in DTYPE:
         raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
-    T, D = x.shape
-    _input(x, "x", (T, D), x.dtype, dev, dense=False)
-    if gamma is not None:
-        _input(gamma, "gamma", (D,), x.dtype, dev)
-    if beta is not None:
-        _input(beta, "beta", (D,), x.dtype, dev)
-    with _on(stream):
-        y = _output(y, "y", (T, D), x.dtype, dev)
-        if want_stats or mean is not None:
-            mean = _output(mean, "mean", (T,), torch.float32, dev)
-        if want_stats or rstd is not None:
-            rstd = _output(rstd, "rstd", (T,), torch.float32, dev)
-    _check(lib().layernorm_fwd(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd), T, D, _ld(x),
-                               float(eps), DTYPE[x.dtype], _stream(stream)))
+    T, D = shape = x.shape
+    px = _input(x, "x", shape, dtype, dev, False)
+    pg = None if gamma is None else _input(gamma, "gamma", (D,), dtype, dev)
+    pb = None if beta is None else _input(beta, "beta", (D,), dtype, dev)
+    y = _output(y, "y", shape, dtype, x)
+    if want_stats or mean is not None:
+        mean = _output(mean, "mean", (T,), torch.float32, x)
+    if want_stats or rstd is not None:
+        rstd = _output(rstd, "rstd", (T,), torch.float32, x)
+    _check(lib().layernorm_fwd(px, pg, pb, y.data_ptr(), _addr(mean), _addr(rstd), T, D, _ld(x), eps, DTYPE[dtype],
+                               stream))
     return y, mean, rstd
+
+
+def layernorm_bwd_workspace_bytes(T: int, D: int, dtype=torch.bfloat16) -> int:
+    return int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[dtype]))
 
 
 def layernorm_bwd(x, dy, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, workspace=None,
@@ -378,70 +413,73 @@ def layernorm_bwd(x, dy, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, wo
     """Layer norm's backward: returns (dx [T, D], dgamma [D] or None, dbeta [D]
     or None).  gamma may be None; there is then no dgamma."""
     dev = _current(x)
-    if x.dim() != 2 or x.dtype not in DTYPE:
+    args = (x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace, want_dgamma, want_dbeta, dev)
+    if stream is not None:
+        with _on(stream, dev) as s:
+            return _layernorm_bwd(*args, s)
+    return _layernorm_bwd(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _layernorm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace, want_dgamma, want_dbeta, dev, stream):
+    dtype = x.dtype
+    if x.dim() != 2 or dtype not in DTYPE:
         raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
-    T, D = x.shape
-    _input(x, "x", (T, D), x.dtype, dev, dense=False)
-    _input(dy, "dy", (T, D), x.dtype, dev, dense=False)
-    if gamma is not None:
-        _input(gamma, "gamma", (D,), x.dtype, dev)
-    _input(mean, "mean", (T,), torch.float32, dev)
-    _input(rstd, "rstd", (T,), torch.float32, dev)
-    nbytes = 0
-    with _on(stream):
-        dx = _output(dx, "dx", (T, D), x.dtype, dev)
-        if dgamma is not None or (want_dgamma and gamma is not None):
-            dgamma = _output(dgamma, "dgamma", (D,), x.dtype, dev)
-        if dbeta is not None or want_dbeta:
-            dbeta = _output(dbeta, "dbeta", (D,), x.dtype, dev)
-        if dgamma is not None or dbeta is not None:
-            nbytes = int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[x.dtype]))
-            workspace = _workspace(workspace, nbytes, dev)
-            nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().layernorm_bwd(_ptr(x), _ptr(dy), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dgamma),
-                               _ptr(dbeta), T, D, _ld(x), _ld(dy), DTYPE[x.dtype], _ptr(workspace), nbytes,
-                               _stream(stream)))
+    T, D = shape = x.shape
+    px = _input(x, "x", shape, dtype, dev, False)
+    py = _input(dy, "dy", shape, dtype, dev, False)
+    pg = None if gamma is None else _input(gamma, "gamma", (D,), dtype, dev)
+    pm = _input(mean, "mean", (T,), torch.float32, dev)
+    pr = _input(rstd, "rstd", (T,), torch.float32, dev)
+    dx = _output(dx, "dx", shape, dtype, x)
+    if dgamma is not None or (want_dgamma and gamma is not None):
+        dgamma = _output(dgamma, "dgamma", (D,), dtype, x)
+    if dbeta is not None or want_dbeta:
+        dbeta = _output(dbeta, "dbeta", (D,), dtype, x)
+    pw, nbytes = None, 0
+    if dgamma is not None or dbeta is not None:
+        workspace = _workspace(workspace, int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[dtype])), x)
+        pw, nbytes = workspace.data_ptr(), workspace.nbytes
+    _check(lib().layernorm_bwd(px, py, pg, pm, pr, dx.data_ptr(), _addr(dgamma), _addr(dbeta), T, D, _ld(x), _ld(dy),
+                               DTYPE[dtype], pw, nbytes, stream))
     return dx, dgamma, dbeta
 
 
-def layernorm_bwd_workspace_bytes(T: int, D: int, dtype=torch.bfloat16) -> int:
-    return int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[dtype]))
-
-
-def _workspace(t, nbytes, device):
-    if t is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    _check_buffer(t, "workspace", nbytes, t.dtype, device)
-    return t
-
-
-def _ffn_inputs(x, w_gate, w_up, act):
-    dev = _current(x)
+def _ffn_inputs(x, w_gate, w_up, act, dev):
+    """Checks the operands of the bf16 projections: ((x, w_gate, w_up), (T, D, F, ld_x, ld_w))."""
     if act not in ACT:
         raise ValueError(f"unknown activation {act!r}")
     if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
         raise ValueError("x must be [T, D] and the weights [F, D]")
-    T, D, F = x.shape[0], x.shape[1], w_gate.shape[0]
-    _input(x, "x", (T, D), torch.bfloat16, dev, dense=False)
-    _input(w_gate, "w_gate", (F, D), torch.bfloat16, dev, dense=False)
-    _input(w_up, "w_up", (F, D), torch.bfloat16, dev, dense=False)
-    if _ld(w_gate) != _ld(w_up):
+    T, D = x.shape
+    F = w_gate.shape[0]
+    ptrs = (_input(x, "x", (T, D), torch.bfloat16, dev, False),
+            _input(w_gate, "w_gate", (F, D), torch.bfloat16, dev, False),
+            _input(w_up, "w_up", (F, D), torch.bfloat16, dev, False))
+    ld_w = _ld(w_gate)
+    if ld_w != _ld(w_up):
         raise ValueError("w_gate and w_up must have the same row stride")
-    return dev, T, D, F
+    return ptrs, (T, D, F, _ld(x), ld_w)
 
 
 def gated_ffn_fwd(x, w_gate, w_up, act: str = "silu", save: bool = False, h=None, gate=None, up=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T) in bf16: returns (h [T, F], gate, up).
     save: keep the projections [T, F] for gated_ffn_bwd (else None); act:
     "silu", "gelu" or "gelu_tanh"."""
-    dev, T, D, F = _ffn_inputs(x, w_gate, w_up, act)
-    with _on(stream):
-        h = _output(h, "h", (T, F), torch.bfloat16, dev)
-        if save or gate is not None or up is not None:
-            gate = _output(gate, "gate", (T, F), torch.bfloat16, dev)
-            up = _output(up, "up", (T, F), torch.bfloat16, dev)
-    _check(lib().gated_ffn_fwd(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(gate), _ptr(up), T, D, F, _ld(x),
-                               _ld(w_gate), ACT[act], _stream(stream)))
+    dev = _current(x)
+    if stream is not None:
+        with _on(stream, dev) as s:
+            return _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, s)
+    return _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, stream):
+    ptrs, dims = _ffn_inputs(x, w_gate, w_up, act, dev)
+    shape = (dims[0], dims[2])
+    h = _output(h, "h", shape, torch.bfloat16, x)
+    if save or gate is not None or up is not None:
+        gate = _output(gate, "gate", shape, torch.bfloat16, x)
+        up = _output(up, "up", shape, torch.bfloat16, x)
+    _check(lib().gated_ffn_fwd(*ptrs, h.data_ptr(), _addr(gate), _addr(up), *dims, ACT[act], stream))
     return h, gate, up
 
 
@@ -453,19 +491,28 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None, dw_
                   workspace=None, want_dx: bool = True, want_dw: bool = True, stream=None):
     """Backward of gated_ffn_fwd from the gate and up it kept: returns
     (dx [T, D], dw_gate [F, D], dw_up [F, D]), None where not wanted."""
-    dev, T, D, F = _ffn_inputs(x, w_gate, w_up, act)
-    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
-        _input(t, name, (T, F), torch.bfloat16, dev)
-    with _on(stream):
-        if want_dx or dx is not None:
-            dx = _output(dx, "dx", (T, D), torch.bfloat16, dev)
-        if want_dw or dw_gate is not None or dw_up is not None:
-            dw_gate = _output(dw_gate, "dw_gate", (F, D), torch.bfloat16, dev)
-            dw_up = _output(dw_up, "dw_up", (F, D), torch.bfloat16, dev)
-        workspace = _workspace(workspace, 4 * T * F, dev)
-    _check(lib().gated_ffn_bwd(_ptr(dh), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(gate), _ptr(up), _ptr(dx),
-                               _ptr(dw_gate), _ptr(dw_up), T, D, F, _ld(x), _ld(w_gate), ACT[act], _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _current(x)
+    args = (dh, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, workspace, want_dx, want_dw, dev)
+    if stream is not None:
+        with _on(stream, dev) as s:
+            return _gated_ffn_bwd(*args, s)
+    return _gated_ffn_bwd(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, workspace, want_dx, want_dw, dev, stream):
+    ptrs, dims = _ffn_inputs(x, w_gate, w_up, act, dev)
+    T, D, F = dims[:3]
+    ph = _input(dh, "dh", (T, F), torch.bfloat16, dev)
+    pg = _input(gate, "gate", (T, F), torch.bfloat16, dev)
+    pu = _input(up, "up", (T, F), torch.bfloat16, dev)
+    if want_dx or dx is not None:
+        dx = _output(dx, "dx", (T, D), torch.bfloat16, x)
+    if want_dw or dw_gate is not None or dw_up is not None:
+        dw_gate = _output(dw_gate, "dw_gate", (F, D), torch.bfloat16, x)
+        dw_up = _output(dw_up, "dw_up", (F, D), torch.bfloat16, x)
+    workspace = _workspace(workspace, gated_ffn_bwd_workspace_bytes(T, F), x)
+    _check(lib().gated_ffn_bwd(ph, *ptrs, pg, pu, _addr(dx), _addr(dw_gate), _addr(dw_up), *dims, ACT[act],
+                               workspace.data_ptr(), workspace.nbytes, stream))
     return dx, dw_gate, dw_up
 
 
@@ -475,28 +522,39 @@ def mxfp8_gated_ffn(a_q, a_s, g_q, g_s, u_q, u_s, T: int, F: int, K: int, act: s
     MMA layout): returns (h bf16 [T, F], None), or with out="e4m3" (codes
     uint8 [T, F], scales uint8), the A operand of the next mxfp8_gemm."""
     dev = _current(a_q)
+    args = (a_q, a_s, g_q, g_s, u_q, u_s, T, F, K, act, out, int(scale_layout), h, h_s, dev)
+    if stream is not None:
+        with _on(stream, dev) as s:
+            return _mxfp8_gated_ffn(*args, s)
+    return _mxfp8_gated_ffn(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _operand(t, name, nbytes, dev):
+    """A contiguous uint8 operand of at least nbytes bytes: its data pointer."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dtype is not torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {nbytes} bytes")
+    return t.data_ptr()
+
+
+def _mxfp8_gated_ffn(a_q, a_s, g_q, g_s, u_q, u_s, T, F, K, act, out, scale_layout, h, h_s, dev, stream):
     if act not in ACT or out not in FFN_OUT:
         raise ValueError(f"unknown activation {act!r} or output {out!r}")
-    for t, name, rows in ((a_q, "a_q", T), (g_q, "g_q", F), (u_q, "u_q", F)):
-        _check_buffer(t, name, rows * K, torch.uint8, dev)
-    for t, name, rows in ((a_s, "a_s", T), (g_s, "g_s", F), (u_s, "u_s", F)):
-        _check_buffer(t, name, scales_bytes(rows, K, SCALES_MMA), torch.uint8, dev)
-        if t is None:
-            raise ValueError(f"{name} is missing")
-    with _on(stream):
-        if out == "bf16":
-            h = _output(h, "h", (T, F), torch.bfloat16, dev)
-            if h_s is not None:
-                raise ValueError("h_s is given for bf16 output")
-        else:
-            h = _output(h, "h", (T, F), torch.uint8, dev)
-            n = scales_bytes(T, F, scale_layout)
-            _check_buffer(h_s, "h_s", n, torch.uint8, dev)
-            if h_s is None:
-                h_s = (torch.empty(T, F // 32, dtype=torch.uint8, device=dev) if scale_layout == SCALES_ROWMAJOR
-                       else torch.zeros(max(n, 1), dtype=torch.uint8, device=dev))
-    _check(lib().mxfp8_gated_ffn(_ptr(a_q), _ptr(a_s), _ptr(g_q), _ptr(g_s), _ptr(u_q), _ptr(u_s), _ptr(h),
-                                 _ptr(h_s), T, F, K, ACT[act], FFN_OUT[out], int(scale_layout), _stream(stream)))
+    s_t, s_f = scales_bytes(T, K, SCALES_MMA), scales_bytes(F, K, SCALES_MMA)
+    ptrs = (_operand(a_q, "a_q", T * K, dev), _operand(a_s, "a_s", s_t, dev), _operand(g_q, "g_q", F * K, dev),
+            _operand(g_s, "g_s", s_f, dev), _operand(u_q, "u_q", F * K, dev), _operand(u_s, "u_s", s_f, dev))
+    if out == "bf16":
+        h = _output(h, "h", (T, F), torch.bfloat16, a_q)
+        if h_s is not None:
+            raise ValueError("h_s is given for bf16 output")
+    else:
+        h = _output(h, "h", (T, F), torch.uint8, a_q)
+        n = scales_bytes(T, F, scale_layout)
+        _check_buffer(h_s, "h_s", n, torch.uint8, a_q.device)
+        if h_s is None:
+            h_s = (a_q.new_empty((T, F // 32)) if scale_layout == SCALES_ROWMAJOR else a_q.new_zeros(max(n, 1)))
+    _check(lib().mxfp8_gated_ffn(*ptrs, h.data_ptr(), _addr(h_s), T, F, K, ACT[act], FFN_OUT[out], scale_layout, stream))
     return h, h_s
 
 
