@@ -795,7 +795,7 @@ int layernorm_fwd(const void* x, const void* gamma, const void* beta, void* y, f
   DeviceInfo dev;
   if ((rc = device_info(&dev))) return rc;
   const char* why = "";
-  const int e = layernorm_fwd_launch(x, gamma, beta, y, mean, rstd, T, (int)D, ld_x, eps, dtype, dev.sms,
+  const int e = layernorm_fwd_launch(x, gamma, beta, y, mean, rstd, T, (int)D, ld_x, eps, dtype, dev.sms, dev.status,
                                      static_cast<cudaStream_t>(stream), &why);
   if (e) return cuda_fail((cudaError_t)e, why);
   return MXN_OK;

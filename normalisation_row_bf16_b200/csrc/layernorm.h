@@ -15,8 +15,8 @@ constexpr int kLnMaxBwdD = 16384;
 // Arguments are checked by the caller (T >= 1, D >= 1, bases 16-byte aligned,
 // ld >= D).  Return 0 or a cudaError_t, with *why naming the failed step.
 int layernorm_fwd_launch(const void* x, const void* gamma, const void* beta, void* y, float* mean, float* rstd,
-                         int64_t T, int D, int64_t ld_x, float eps, int dtype, int sms, cudaStream_t stream,
-                         const char** why);
+                         int64_t T, int D, int64_t ld_x, float eps, int dtype, int sms, unsigned* status,
+                         cudaStream_t stream, const char** why);
 
 size_t layernorm_bwd_workspace(int64_t T, int D, int dtype, int sms);
 
