@@ -19,6 +19,8 @@
 // as an MN-major operand, so nothing is transposed in memory.
 #include "gated_ffn.h"
 
+#include <mutex>
+
 #include "activations.cuh"
 #include "tcgen05.cuh"
 
@@ -27,22 +29,34 @@ namespace {
 
 enum Mode { kGate, kDx, kDw };
 
-constexpr int kTileM = 128;                      // output rows of a tile
+// Tile shapes (see the kernel): one CTA, 128 x tile_n; a pair of CTAs, 256 x 256
+// with two accumulators; a pair of CTAs, 512 x 256 in two accumulators.
+enum Kind { kSingle, kPair, kWide };
+
 constexpr int kTileK = 64;                       // contraction elements (128 bytes) per stage
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;                     // 4 lane quarters x 2 column halves
 constexpr int kThreads = 64 + 32 * kEpiWarps;    // producer warp, MMA warp, epilogue warps
-constexpr uint32_t kABytes = kTileM * kTileK * 2;
+constexpr uint32_t kABytes = 128 * kTileK * 2;   // 128 rows of A
 constexpr uint32_t kTmemCols = 512;              // two accumulators of up to 256 columns
+constexpr uint32_t kBoxBytes = 32 * 128;         // a store box: 32 rows x 64 columns
 constexpr int kGroupM = 8;                       // tiles go m-first inside groups of 8 tile rows: operand reuse in L2
 
+// Store boxes an epilogue warp of a pair holds: h, gate and up; else one.
+__host__ __device__ constexpr int boxes(int mode, int kind) {
+  return kind == kSingle ? 0 : (mode == kGate ? 3 : 1);
+}
+
 struct Args {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[2], b[2], c[3];                  // c: outputs, of pairs
   uint16_t* out[3];      // kGate: h, gate, up (the last two may be null); kDx: dx; kDw: dWg, dWu
   unsigned* status;
   int64_t ld_out;
+  int problems;
   int M, N;              // output rows and columns of one problem
-  int m_tiles, n_tiles, tiles;   // tiles: of all problems
+  int m_tiles, n_tiles;  // tiles of one problem (kWide: 512-row tiles that are whole 256-row halves)
+  int tiles, wide;       // work units of all problems; kWide: those that are whole 512-row tiles
+  int m_halves;          // kWide: 256-row halves of one problem
   int n_k, n_k0;         // K stages of a tile, and of its first segment (kDx)
   int tile_n;            // output columns of a tile (kGate: features, each with a gate and an up column)
   int acc_n;             // accumulator columns: 2 * tile_n (kGate) or tile_n
@@ -58,19 +72,64 @@ struct Barriers {
   uint32_t tmem_base;
   uint32_t failed;
 };
+static_assert(sizeof(Barriers) <= 512, "barrier block");
+constexpr size_t kSmemCap = 227 * 1024 - 512;    // ring and store boxes
 
 __device__ __forceinline__ bool failed_flag(const Barriers& S) {
   return *reinterpret_cast<const volatile uint32_t*>(&S.failed) != 0;
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 2-D tensor copy into this CTA's shared memory, completing on the barrier at
+// shared::cluster address `bar` (of a pair, CTA 0's).
+template <bool PAIR>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (PAIR)
+    tma_load_2d_pair(dst, map, x, y, bar);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// All 512 columns of tensor memory, by one warp (of each CTA of a pair).
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t* base) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(base)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(base)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t tmem) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator (bit 4), A and B bf16
@@ -114,21 +173,47 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Tile t of the launch -> problem, tile row, tile column.
+// Work unit t of the launch: problem, first output row, tile column, and for
+// kWide the 256-row halves it covers.
+// kWide: units of the last 256-row half when there is an odd number of them.
+__host__ __device__ __forceinline__ int odd_halves(const Args& A) {
+  return A.m_halves & 1 ? A.problems * A.n_tiles : 0;
+}
 struct TilePos {
-  int p, mt, nt;
+  int p, m0, nt, halves;
 };
-__device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
+__device__ __forceinline__ TilePos tile_of(const Args& A, int t, int rows) {
   TilePos q;
   const int per = A.m_tiles * A.n_tiles;
   q.p = t / per;
   t -= q.p * per;
   const int span = kGroupM * A.n_tiles;
-  const int m0 = t / span * kGroupM;
-  const int gm = min(kGroupM, A.m_tiles - m0);
-  t -= m0 * A.n_tiles;
-  q.mt = m0 + t % gm;
+  const int g0 = t / span * kGroupM;
+  const int gm = min(kGroupM, A.m_tiles - g0);
+  t -= g0 * A.n_tiles;
+  q.m0 = (g0 + t % gm) * rows;
   q.nt = t / gm;
+  q.halves = 2;
+  return q;
+}
+template <int KIND>
+__device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
+  if constexpr (KIND != kWide) return tile_of(A, t, KIND == kPair ? 256 : 128);
+  if (t < A.wide) return tile_of(A, t, 512);
+  // The tiles past the last full round, as halves; then the odd half row.
+  const int all = A.tiles == A.wide ? 0 : (A.tiles - A.wide - odd_halves(A)) / 2;
+  t -= A.wide;
+  TilePos q;
+  if (t < 2 * all) {
+    q = tile_of(A, A.wide + t / 2, 512);
+    q.m0 += (t & 1) * 256;
+  } else {
+    t -= 2 * all;
+    q.p = t / A.n_tiles;
+    q.nt = t - q.p * A.n_tiles;
+    q.m0 = (A.m_halves - 1) * 256;
+  }
+  q.halves = 1;
   return q;
 }
 
@@ -138,24 +223,72 @@ __device__ __forceinline__ void store_cols16(uint16_t* row, int col, int n, cons
   if (col + 8 < n) *reinterpret_cast<uint4*>(row + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+__device__ __forceinline__ void pack16(const uint32_t (&r)[16], uint32_t (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
 template <int ACT>
-__device__ __forceinline__ void gate_product(const uint32_t (&g)[16], const uint32_t (&u)[16], uint32_t (&o)[8]) {
+__device__ __forceinline__ void gate_product_of(const uint32_t (&g)[16], const uint32_t (&u)[16], uint32_t (&o)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     o[i] = pack_bf16(act_f<ACT>(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
                      act_f<ACT>(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
 }
+__device__ __forceinline__ void gate_product(int act, const uint32_t (&g)[16], const uint32_t (&u)[16], uint32_t (&o)[8]) {
+  if (act == kActSilu) gate_product_of<kActSilu>(g, u, o);
+  else if (act == kActGelu) gate_product_of<kActGelu>(g, u, o);
+  else gate_product_of<kActGeluTanh>(g, u, o);
+}
+
+// 2-D tensor copy shared -> global of a store box (clipped at the tensor's
+// edges), tracked by the issuing thread's bulk groups.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+               "r"(smem_u32(src))
+               : "memory");
+}
 
 // Persistent CTAs, one per SM, walk the output tiles.  Warp 0 streams K stages
 // of both operands into a shared-memory ring with TMA tensor copies (out of
-// range rows and columns arrive as zeros); warp 1 issues tcgen05.mma into one
-// of two accumulators; warps 2..9 drain the other.  Every wait is bounded, as
-// in gemm_mxfp8.cu.
-template <int MODE>
+// range rows and columns arrive as zeros); warp 1 issues tcgen05.mma; warps
+// 2..9 drain the accumulators.  Every wait is bounded, as in gemm_mxfp8.cu.
+//
+// kSingle: one CTA, 128 rows x tile_n columns, two accumulators in turn, direct
+// stores -- few rows, where many narrow tiles stream the weights.
+// kPair: two CTAs (a cluster on two SMs) share a 256 x 256 tile.  Each loads its
+// 128 rows of A and half of B's 256 -- in kGate CTA 0 the gate rows and CTA 1
+// the up rows of the tile's 128 features, so both accumulators hold both --
+// and CTA 0 issues tcgen05.mma.cta_group::2 for the pair.  Two accumulators in
+// turn hide the epilogue, whose results leave through shared memory as 32 x 64
+// boxes by TMA: direct 16-byte stores of h, gate and up cost 180 of 1520 us at
+// 8192 x 4096 x 14336.
+// kWide: as kPair with 512 x 256 tiles: two M = 256 MMAs a K step on one B, a
+// quarter fewer operand bytes per product (the tensor cores wait for operands:
+// the 256 x 256 backward products ran 2766 us, 2346 with the copies left out).
+// Both accumulators fill at once, so a tile's epilogue is exposed except that
+// the next tile's first ring of stages goes to the first accumulator while the
+// second still drains; the contractions of the backward are long.  Tiles past
+// the last full round of pairs are dealt as 256-row halves.
+// Copies of both CTAs of a pair complete on CTA 0's barriers, one
+// tcgen05.commit per CTA frees the stages, and no copy is multicast.
+template <int MODE, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_constant__ Args A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Barriers& S = *reinterpret_cast<Barriers*>(smem_raw + (size_t)A.stages * A.stage_bytes);
+  constexpr bool PAIR = KIND != kSingle;
+  if constexpr (PAIR) {
+    // Without a two-CTA cluster the paired allocation would wait for a partner that does not exist.
+    if (cluster_size() != 2) {
+      if (threadIdx.x == 0) atomicOr(A.status, kStatusWaitTimeout);
+      return;
+    }
+  }
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int first = PAIR ? (int)cluster_id_x() : (int)blockIdx.x, step = PAIR ? (int)n_clusters_x() : (int)gridDim.x;
+  uint8_t* store_box = smem_raw + (size_t)A.stages * A.stage_bytes;
+  Barriers& S = *reinterpret_cast<Barriers*>(store_box + (size_t)kEpiWarps * boxes(MODE, KIND) * kBoxBytes);
   constexpr bool kAmn = MODE == kDw, kBmn = MODE != kGate;
+  constexpr uint32_t kAHalf = kABytes;           // kWide: a stage holds two 128-row blocks of A, then B
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -165,21 +298,17 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&S.acc_full[b], 1);
-      mbar_init(&S.acc_empty[b], kEpiWarps);
+      mbar_init(&S.acc_empty[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(&S.mma_done, 1);
     S.failed = 0;
     fence_barrier_init();
   }
   __syncwarp();
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc<PAIR>(&S.tmem_base);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();        // both CTAs' barriers and allocation are in place
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   griddep_wait();
@@ -191,8 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
       // ---------------------------------------------------------- producer
       uint32_t s = 0, ph = 1;
       bool ok = true;
-      for (int t = blockIdx.x; t < A.tiles && ok; t += gridDim.x) {
-        const TilePos q = tile_pos(A, t);
+      for (int t = first; t < A.tiles && ok; t += step) {
+        const TilePos q = tile_pos<KIND>(A, t);
+        // bytes of a stage: kWide tiles of one half leave A's second block out
+        const uint32_t bytes = KIND == kWide && q.halves == 1 ? A.stage_bytes - kAHalf : A.stage_bytes;
         for (int kb = 0; kb < A.n_k; ++kb) {
           if (!mbar_wait_bounded(&S.empty[s], ph, A.status) || failed_flag(S)) {
             atomicOr(&S.failed, 1u);
@@ -200,20 +331,32 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             break;
           }
           uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes;
-          uint8_t* sb = sa + kABytes;
-          uint64_t* bar = &S.full[s];
-          mbar_arrive_expect_tx(bar, A.stage_bytes);
+          uint8_t* sb = sa + (KIND == kWide ? 2 * kAHalf : kABytes);
+          const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * bytes : bytes);
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) { tma_load<PAIR>(dst, map, x, y, bar); };
           if constexpr (MODE == kGate) {
-            tma_load_2d(sa, &A.a[0], kb * kTileK, q.mt * kTileM, bar);
-            tma_load_2d(sb, &A.b[0], kb * kTileK, q.nt * A.tile_n, bar);
-            tma_load_2d(sb + A.tile_n * 128, &A.b[1], kb * kTileK, q.nt * A.tile_n, bar);
-          } else if constexpr (MODE == kDx) {
-            const int seg = kb >= A.n_k0, k0 = (kb - seg * A.n_k0) * kTileK;
-            tma_load_2d(sa, &A.a[seg], k0, q.mt * kTileM, bar);
-            for (int c = 0; c < A.tile_n; c += 64) tma_load_2d(sb + c * 128, &A.b[seg], q.nt * A.tile_n + c, k0, bar);
+            load(sa, &A.a[0], kb * kTileK, q.m0 + (int)rank * 128);
+            if constexpr (PAIR) {
+              load(sb, &A.b[rank], kb * kTileK, q.nt * A.tile_n);
+            } else {
+              load(sb, &A.b[0], kb * kTileK, q.nt * A.tile_n);
+              load(sb + A.tile_n * 128, &A.b[1], kb * kTileK, q.nt * A.tile_n);
+            }
           } else {
-            for (int c = 0; c < kTileM; c += 64) tma_load_2d(sa + c * 128, &A.a[q.p], q.mt * kTileM + c, kb * kTileK, bar);
-            for (int c = 0; c < A.tile_n; c += 64) tma_load_2d(sb + c * 128, &A.b[0], q.nt * A.tile_n + c, kb * kTileK, bar);
+            const int n0 = q.nt * A.tile_n + (PAIR ? (int)rank * 128 : 0), nb = PAIR ? 128 : A.tile_n;
+            const int blocks = KIND == kWide ? q.halves : 1;
+            const int seg = MODE == kDx && kb >= A.n_k0, k0 = (kb - seg * A.n_k0) * kTileK;
+            for (int h = 0; h < blocks; ++h) {
+              const int m = q.m0 + h * 256 + (int)rank * 128;
+              if constexpr (MODE == kDx) {
+                load(sa + h * kAHalf, &A.a[seg], k0, m);
+              } else {
+                load(sa + h * kAHalf, &A.a[q.p], m, k0);
+                load(sa + h * kAHalf + kAHalf / 2, &A.a[q.p], m + 64, k0);
+              }
+            }
+            for (int c = 0; c < nb; c += 64) load(sb + c * 128, &A.b[seg], n0 + c, k0);
           }
           ++n_issued;
           if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
@@ -221,109 +364,222 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------- MMA
-      uint32_t s = 0, ph = 0, it = 0;
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------ MMA (of a pair: CTA 0)
+      uint32_t s = 0, ph = 0, it = 0, uses[2] = {0, 0};
       bool ok = true;
-      const uint32_t idesc = instr_desc(kTileM, A.acc_n, kAmn, kBmn);
-      for (int t = blockIdx.x; t < A.tiles && ok; t += gridDim.x, ++it) {
-        const uint32_t buf = it & 1u;
-        if (!mbar_wait_bounded(&S.acc_empty[buf], ((it >> 1) & 1u) ^ 1u, A.status) || failed_flag(S)) {
+      const uint32_t idesc = instr_desc(PAIR ? 256 : 128, A.acc_n, kAmn, kBmn);
+      auto commit = [&](uint64_t* bar) {         // to both CTAs of a pair
+        if constexpr (PAIR) {
+          tc_commit_pair(smem_u32(bar));
+          tc_commit_pair(cluster_addr(bar, 1));
+        } else {
+          tc_commit(bar);
+        }
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && (!mbar_wait_bounded(bar, parity, A.status) || failed_flag(S))) {
           atomicOr(&S.failed, 1u);
           ok = false;
-          break;
         }
         tc_fence_after();
-        for (int kb = 0; kb < A.n_k; ++kb) {
-          if (!mbar_wait_bounded(&S.full[s], ph, A.status) || failed_flag(S)) {
-            atomicOr(&S.failed, 1u);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(smem_raw) + s * A.stage_bytes, b0 = a0 + kABytes;
+      };
+      // One stage into accumulator `acc`, from the h-th block of A.
+      auto mma_stage = [&](uint32_t stage, int h, uint32_t acc, bool first_k) {
+        const uint32_t a0 = smem_u32(smem_raw) + stage * A.stage_bytes + (uint32_t)h * kAHalf;
+        const uint32_t b0 = smem_u32(smem_raw) + stage * A.stage_bytes + (KIND == kWide ? 2 * kAHalf : kABytes);
 #pragma unroll
-          for (int k = 0; k < kTileK / 16; ++k)
-            mma_bf16(tmem + buf * 256u, op_desc(a0, k, kAmn), op_desc(b0, k, kBmn), idesc, (kb > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&S.empty[s]);
-          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
+        for (int k = 0; k < kTileK / 16; ++k)
+          mma_bf16<PAIR>(tmem + acc * 256u, op_desc(a0, k, kAmn), op_desc(b0, k, kBmn), idesc, (!first_k || k > 0) ? 1u : 0u);
+      };
+      for (int t = first; t < A.tiles && ok; t += step, ++it) {
+        if constexpr (KIND != kWide) {
+          const uint32_t acc = it & 1u;
+          wait(&S.acc_empty[acc], (uses[acc]++ & 1u) ^ 1u);
+          for (int kb = 0; kb < A.n_k && ok; ++kb) {
+            wait(&S.full[s], ph);
+            if (!ok) break;
+            mma_stage(s, 0, acc, kb == 0);
+            commit(&S.empty[s]);
+            if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
+          }
+          if (ok) commit(&S.acc_full[acc]);
+        } else {
+          const int halves = tile_pos<KIND>(A, t).halves;
+          const int lead = halves == 2 ? min(A.n_k, A.stages) : 0;   // stages that go to the first accumulator alone
+          wait(&S.acc_empty[0], (uses[0]++ & 1u) ^ 1u);
+          uint32_t s1 = s;
+          for (int kb = 0; kb < lead && ok; ++kb) {
+            wait(&S.full[s], ph);
+            if (!ok) break;
+            mma_stage(s, 0, 0, kb == 0);
+            if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
+          }
+          if (halves == 2) {
+            wait(&S.acc_empty[1], (uses[1]++ & 1u) ^ 1u);
+            for (int kb = 0; kb < lead && ok; ++kb) {
+              mma_stage(s1, 1, 1, kb == 0);
+              commit(&S.empty[s1]);
+              if (++s1 == (uint32_t)A.stages) s1 = 0;
+            }
+          }
+          for (int kb = lead; kb < A.n_k && ok; ++kb) {
+            wait(&S.full[s], ph);
+            if (!ok) break;
+            mma_stage(s, 0, 0, kb == 0);
+            if (halves == 2) mma_stage(s, 1, 1, kb == 0);
+            commit(&S.empty[s]);
+            if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
+          }
+          if (ok) commit(&S.acc_full[0]);
+          if (ok && halves == 2) commit(&S.acc_full[1]);
         }
-        if (ok) tc_commit(&S.acc_full[buf]);
       }
-      tc_commit(&S.mma_done);
-      if (!ok) {                                 // wake the epilogue; it sees the failure
-        tc_commit(&S.acc_full[0]);
-        tc_commit(&S.acc_full[1]);
+      if constexpr (PAIR) tc_commit_pair(smem_u32(&S.mma_done));
+      else tc_commit(&S.mma_done);
+      if (!ok) {                                 // wake the epilogues; they see the failure or time out
+        commit(&S.acc_full[0]);
+        commit(&S.acc_full[1]);
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;                // tcgen05.ld reaches lanes 32 * (warp % 4) ..
-    const int half = (warp - 2) >> 2;            // 16-column chunks half, half + 2, ..
-    uint32_t it = 0;
-    for (int t = blockIdx.x; t < A.tiles; t += gridDim.x, ++it) {
-      const TilePos q = tile_pos(A, t);
-      const uint32_t buf = it & 1u;
-      const bool got = mbar_wait_bounded(&S.acc_full[buf], (it >> 1) & 1u, A.status);
-      tc_fence_after();
-      if (!got || failed_flag(S)) {
-        if (lane == 0) atomicOr(&S.failed, 1u);
-        break;
-      }
-      const int row = q.mt * kTileM + quarter * 32 + lane;
-      const bool live = row < A.M;
-      const uint32_t ta = tmem + buf * 256u + ((uint32_t)(quarter * 32) << 16);
-      for (int c = half * 16; c < A.tile_n; c += 32) {
-        const int col = q.nt * A.tile_n + c;
-        uint32_t r[16], o[8];
-        tmem_ld16(ta + (uint32_t)c, r);
-        if constexpr (MODE == kGate) {
-          uint32_t u[16];
-          tmem_ld16(ta + (uint32_t)(A.tile_n + c), u);
-          tmem_ld16_fence(r, true);
-          tmem_ld16_fence(u, false);
-          if (A.act == kActSilu) gate_product<kActSilu>(r, u, o);
-          else if (A.act == kActGelu) gate_product<kActGelu>(r, u, o);
-          else gate_product<kActGeluTanh>(r, u, o);
-          if (live) {
-            store_cols16(A.out[0] + (int64_t)row * A.ld_out, col, A.N, o);
-            if (A.out[1]) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-              store_cols16(A.out[1] + (int64_t)row * A.ld_out, col, A.N, o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-              store_cols16(A.out[2] + (int64_t)row * A.ld_out, col, A.N, o);
+    const int half = (warp - 2) >> 2;
+    uint8_t* box = store_box + (size_t)(warp - 2) * boxes(MODE, KIND) * kBoxBytes;
+    // 8 columns (16 bytes) of this lane's row in a store box: 128-byte swizzle
+    auto put = [&](int b, int col8, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+      sts128(smem_u32(box) + (uint32_t)b * kBoxBytes + 128u * lane + 16u * (col8 ^ (lane & 7)), make_uint4(x, y, z, w));
+    };
+    uint32_t it = 0, uses[2] = {0, 0};
+    bool ok = true;
+    for (int t = first; t < A.tiles && ok; t += step, ++it) {
+      const TilePos q = tile_pos<KIND>(A, t);
+      for (int a = 0; a < (KIND == kWide ? q.halves : 1) && ok; ++a) {
+        const uint32_t acc = KIND == kWide ? (uint32_t)a : (it & 1u);
+        const bool got = mbar_wait_bounded(&S.acc_full[acc], uses[acc]++ & 1u, A.status);
+        tc_fence_after();
+        if (!got || failed_flag(S)) {
+          if (lane == 0) atomicOr(&S.failed, 1u);
+          ok = false;
+          break;
+        }
+        const int row0 = q.m0 + a * 256 + (int)rank * 128 + quarter * 32;
+        const uint32_t ta = tmem + acc * 256u + ((uint32_t)(quarter * 32) << 16);
+        if constexpr (KIND == kSingle) {
+          const int row = row0 + lane;
+          const bool live = row < A.M;
+          for (int c = half * 16; c < A.tile_n; c += 32) {
+            const int col = q.nt * A.tile_n + c;
+            uint32_t r[16], o[8];
+            tmem_ld16(ta + (uint32_t)c, r);
+            if constexpr (MODE == kGate) {
+              uint32_t u[16];
+              tmem_ld16(ta + (uint32_t)(A.tile_n + c), u);
+              tmem_ld16_fence(r, true);
+              tmem_ld16_fence(u, false);
+              gate_product(A.act, r, u, o);
+              if (live) {
+                store_cols16(A.out[0] + (int64_t)row * A.ld_out, col, A.N, o);
+                if (A.out[1]) {
+                  pack16(r, o);
+                  store_cols16(A.out[1] + (int64_t)row * A.ld_out, col, A.N, o);
+                  pack16(u, o);
+                  store_cols16(A.out[2] + (int64_t)row * A.ld_out, col, A.N, o);
+                }
+              }
+            } else {
+              tmem_ld16_fence(r, true);
+              pack16(r, o);
+              if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, A.N, o);
             }
+            __syncwarp();                        // tcgen05.ld needs the warp converged
+          }
+        } else if constexpr (MODE == kGate) {
+          // 64 features a warp: h, and gate and up when kept
+          const int col0 = q.nt * A.tile_n + half * 64;
+          const bool keep = A.out[1] != nullptr;
+          if (lane == 0) bulk_wait_read_all();   // the boxes of the tile before have left
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t r[16], u[16], o[8];
+            tmem_ld16(ta + (uint32_t)(half * 64 + c), r);
+            tmem_ld16(ta + (uint32_t)(128 + half * 64 + c), u);
+            tmem_ld16_fence(r, true);
+            tmem_ld16_fence(u, false);
+            gate_product(A.act, r, u, o);
+            put(0, c / 8, o[0], o[1], o[2], o[3]);
+            put(0, c / 8 + 1, o[4], o[5], o[6], o[7]);
+            if (keep) {
+              pack16(r, o);
+              put(1, c / 8, o[0], o[1], o[2], o[3]);
+              put(1, c / 8 + 1, o[4], o[5], o[6], o[7]);
+              pack16(u, o);
+              put(2, c / 8, o[0], o[1], o[2], o[3]);
+              put(2, c / 8 + 1, o[4], o[5], o[6], o[7]);
+            }
+            __syncwarp();
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row0 < A.M && col0 < A.N) {
+            for (int b = 0; b < (keep ? 3 : 1); ++b) tma_store_2d(&A.c[b], box + b * kBoxBytes, col0, row0);
+            bulk_commit();
           }
         } else {
-          tmem_ld16_fence(r, true);
+          // 128 columns a warp, in two boxes through one buffer
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-          if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, A.N, o);
+          for (int v = 0; v < 2; ++v) {
+            const int col0 = q.nt * A.tile_n + half * 128 + v * 64;
+            uint32_t r[4][16], o[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld16(ta + (uint32_t)(half * 128 + v * 64 + 16 * c), r[c]);
+            tmem_ld16_fence(r[0], true);
+#pragma unroll
+            for (int c = 1; c < 4; ++c) tmem_ld16_fence(r[c], false);
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              pack16(r[c], o);
+              put(0, 2 * c, o[0], o[1], o[2], o[3]);
+              put(0, 2 * c + 1, o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < A.M && col0 < A.N) {
+              tma_store_2d(&A.c[MODE == kDw ? q.p : 0], box, col0, row0);
+              bulk_commit();
+            }
+          }
         }
-        __syncwarp();                            // tcgen05.ld needs the warp converged
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {                         // the MMA thread may overwrite this accumulator
+          if (rank == 0) mbar_arrive(&S.acc_empty[acc]);
+          else mbar_arrive_remote(cluster_addr(&S.acc_empty[acc], 0));
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.acc_empty[buf]);
     }
+    if (PAIR && lane == 0) bulk_wait_read_all(); // before the CTA's shared memory goes
   }
 
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 1 && lane == 0) mbar_wait_bounded(&S.mma_done, 0, A.status);
-  // After a wait gave up, leave no copy in flight: the producer waits (bounded)
-  // for the last issued phase of every stage.
-  if (warp == 0 && lane == 0 && failed_flag(S))
+  if (warp == 1 && lane == 0 && rank == 0) mbar_wait_bounded(&S.mma_done, 0, A.status);
+  // After a wait gave up, leave no copy in flight: the producer (of a pair, CTA
+  // 0's, where both CTAs' copies complete) waits, bounded, for the last issued
+  // phase of every stage.
+  if (warp == 0 && lane == 0 && rank == 0 && failed_flag(S))
     for (uint32_t j = (n_issued > (uint32_t)A.stages ? n_issued - A.stages : 0); j < n_issued; ++j)
       mbar_wait_bounded(&S.full[j % A.stages], (j / A.stages) & 1u, A.status);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();        // no MMA, copy or remote arrive into either CTA remains
   tc_fence_after();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  if (warp == 0) tmem_free<PAIR>(tmem);
 }
 
 // dg = dh * up * act'(gate), du = dh * act(gate): 8 elements a thread and step.
@@ -371,17 +627,21 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, in
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int launch_pdl(const void* kernel, int grid, int threads, size_t smem, void** argv, cudaStream_t stream,
-               const char* what, const char** why) {
+               const char* what, const char** why, bool pair = false) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pair ? 2 : 1;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) { *why = cudaGetErrorString(e); return (int)e; }
@@ -391,39 +651,124 @@ int launch_pdl(const void* kernel, int grid, int threads, size_t smem, void** ar
   return 0;
 }
 
-// Fills the tile and ring geometry of a launch.  Tile widths that divide the
-// columns over the SMs in the fewest rounds of equal cost: with m_tiles tile
-// rows, the candidate with the least (rounds x columns a tile).
-// Returns false when the tiles outnumber an int.
-bool plan_tiles(Args& A, int mode, int problems, int sms) {
-  A.m_tiles = cdiv(A.M, kTileM);
+// Pairs of CTAs of a kernel that fit on the device at once (0 if none), looked
+// up once per device and kernel.
+int pair_capacity(const void* kernel, int mode, size_t smem) {
+  static std::mutex mu;
+  static int cached[64][3];                      // pairs + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  if (cached[dev][mode]) return cached[dev][mode] - 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  cached[dev][mode] = n + 1;
+  return n;
+}
+
+struct Launch {
+  const void* kernel;
+  int kind, grid;
+  size_t smem;
+};
+
+const void* kernel_of(int mode, int kind) {
+  if (mode == kGate)
+    return kind == kSingle ? (const void*)gated_gemm_kernel<kGate, kSingle> : (const void*)gated_gemm_kernel<kGate, kPair>;
+  if (mode == kDx)
+    return kind == kSingle ? (const void*)gated_gemm_kernel<kDx, kSingle> : (const void*)gated_gemm_kernel<kDx, kWide>;
+  return kind == kSingle ? (const void*)gated_gemm_kernel<kDw, kSingle> : (const void*)gated_gemm_kernel<kDw, kWide>;
+}
+
+// Fills the tile and ring geometry of a launch.  Returns false when the tiles
+// outnumber an int.
+bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   const int unit = mode == kGate ? 16 : 64, widest = mode == kGate ? 128 : 256;
+  const int wide_kind = mode == kGate ? kPair : kWide;
+  A.problems = problems;
+  // Single CTAs: the tile width that divides the columns over the SMs in the
+  // fewest rounds of equal cost; a tile costs its columns, and its 128 rows of
+  // A once more.
   int64_t best = 0;
   for (int w = widest; w >= unit; w -= unit) {
-    const int64_t tiles = (int64_t)A.m_tiles * cdiv(A.N, w) * problems;
-    // A tile costs its columns, and its 128 rows of A once more.
+    const int64_t tiles = (int64_t)cdiv(A.M, 128) * cdiv(A.N, w) * problems;
     const int64_t cost = ((tiles + sms - 1) / sms) * ((mode == kGate ? 2 * w : w) + 64);
     if (best == 0 || cost < best) {
       best = cost;
       A.tile_n = w;
     }
   }
+  L->kind = kSingle;
+  // Pairs.
+  const uint32_t pair_stage = (wide_kind == kWide ? 3 : 2) * kABytes;
+  const size_t pair_boxes = (size_t)kEpiWarps * boxes(mode, wide_kind) * kBoxBytes;
+  const int pair_stages = (int)((kSmemCap - pair_boxes) / pair_stage);
+  const size_t pair_smem = (size_t)pair_stages * pair_stage + pair_boxes + sizeof(Barriers);
+  int pairs = 0;
+  if (A.M > 128) {
+    pairs = pair_capacity(kernel_of(mode, wide_kind), mode, pair_smem);
+    if (pairs > sms / 2) pairs = sms / 2;
+    const int64_t tiles = (int64_t)cdiv(A.M, 256) * cdiv(A.N, widest) * problems;
+    const int64_t cost = pairs ? ((tiles + pairs - 1) / pairs) * 256 : best;
+    if (cost < best) {
+      L->kind = wide_kind;
+      A.tile_n = widest;
+    }
+  }
   A.n_tiles = cdiv(A.N, A.tile_n);
-  const int64_t tiles = (int64_t)A.m_tiles * A.n_tiles * problems;
+  A.m_tiles = cdiv(A.M, L->kind == kSingle ? 128 : 256);
+  A.m_halves = A.m_tiles;
+  int64_t tiles = (int64_t)A.m_tiles * A.n_tiles * problems;
   if (tiles > 0x7FFFFFFF - sms) return false;
+  int units = L->kind == kSingle ? sms : pairs;
+  if (L->kind == kWide) {
+    A.m_tiles = A.m_halves / 2;
+    const int64_t whole = (int64_t)A.m_tiles * A.n_tiles * problems, odd = (A.m_halves & 1) * A.n_tiles * (int64_t)problems;
+    const int64_t rest = whole % pairs;          // past the last full round
+    A.wide = (int)(2 * rest + odd <= pairs ? whole - rest : whole);
+    tiles = A.wide + 2 * (whole - A.wide) + odd;
+  }
   A.tiles = (int)tiles;
   A.acc_n = mode == kGate ? 2 * A.tile_n : A.tile_n;
-  A.stage_bytes = kABytes + (uint32_t)A.acc_n * 128u;
-  const size_t cap = 227 * 1024 - sizeof(Barriers);
-  A.stages = (int)(cap / A.stage_bytes);
-  if (A.stages > kMaxStages) A.stages = kMaxStages;
+  if (L->kind == kSingle) {
+    A.stage_bytes = kABytes + (uint32_t)A.acc_n * 128u;
+    A.stages = (int)(kSmemCap / A.stage_bytes);
+    if (A.stages > kMaxStages) A.stages = kMaxStages;
+    L->smem = (size_t)A.stages * A.stage_bytes + sizeof(Barriers);
+  } else {
+    A.stage_bytes = pair_stage;
+    A.stages = pair_stages;
+    L->smem = pair_smem;
+  }
+  L->kernel = kernel_of(mode, L->kind);
+  L->grid = (A.tiles < units ? A.tiles : units) * (L->kind == kSingle ? 1 : 2);
   return true;
 }
 
-int launch_gemm(const void* kernel, Args& A, int sms, cudaStream_t stream, const char* what, const char** why) {
+int launch_gemm(const Launch& L, Args& A, cudaStream_t stream, const char* what, const char** why) {
   void* argv[] = {&A};
-  const size_t smem = (size_t)A.stages * A.stage_bytes + sizeof(Barriers);
-  return launch_pdl(kernel, A.tiles < sms ? A.tiles : sms, kThreads, smem, argv, stream, what, why);
+  return launch_pdl(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.kind != kSingle);
+}
+
+// Maps of the outputs (bf16 [rows, cols] dense) for store boxes.
+bool make_out_maps(Args& A) {
+  for (int i = 0; i < 3; ++i)
+    if (A.out[i] && !make_map(&A.c[i], A.out[i], A.M, A.N, A.ld_out, 32)) return false;
+  return true;
 }
 
 }  // namespace
@@ -441,13 +786,14 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
   A.N = F;
   A.act = act;
   A.n_k = A.n_k0 = cdiv(D, kTileK);
-  if (!plan_tiles(A, kGate, 1, sms)) { *why = "too many tiles"; return -1; }
-  if (!make_map(&A.a[0], x, T, D, ld_x, kTileM) || !make_map(&A.b[0], w_gate, F, D, ld_w, A.tile_n) ||
-      !make_map(&A.b[1], w_up, F, D, ld_w, A.tile_n)) {
+  Launch L;
+  if (!plan_tiles(A, kGate, 1, sms, &L)) { *why = "too many tiles"; return -1; }
+  if (!make_map(&A.a[0], x, T, D, ld_x, 128) || !make_map(&A.b[0], w_gate, F, D, ld_w, A.tile_n) ||
+      !make_map(&A.b[1], w_up, F, D, ld_w, A.tile_n) || (L.kind != kSingle && !make_out_maps(A))) {
     *why = "cuTensorMapEncodeTiled failed";
     return -1;
   }
-  return launch_gemm((const void*)gated_gemm_kernel<kGate>, A, sms, stream, "gated_ffn_fwd launch", why);
+  return launch_gemm(L, A, stream, "gated_ffn_fwd launch", why);
 }
 
 int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
@@ -474,13 +820,15 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     A.N = D;
     A.n_k0 = cdiv(F, kTileK);
     A.n_k = 2 * A.n_k0;
-    if (!plan_tiles(A, kDx, 1, sms)) { *why = "too many tiles"; return -1; }
-    if (!make_map(&A.a[0], dg, T, F, F, kTileM) || !make_map(&A.a[1], du, T, F, F, kTileM) ||
-        !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK)) {
+    Launch L;
+    if (!plan_tiles(A, kDx, 1, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (!make_map(&A.a[0], dg, T, F, F, 128) || !make_map(&A.a[1], du, T, F, F, 128) ||
+        !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK) ||
+        (L.kind != kSingle && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";
       return -1;
     }
-    e = launch_gemm((const void*)gated_gemm_kernel<kDx>, A, sms, stream, "gated_ffn_bwd dx launch", why);
+    e = launch_gemm(L, A, stream, "gated_ffn_bwd dx launch", why);
     if (e) return e;
   }
   if (dw_gate) {
@@ -492,13 +840,14 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     A.M = F;
     A.N = D;
     A.n_k = A.n_k0 = cdiv(T, kTileK);
-    if (!plan_tiles(A, kDw, 2, sms)) { *why = "too many tiles"; return -1; }
+    Launch L;
+    if (!plan_tiles(A, kDw, 2, sms, &L)) { *why = "too many tiles"; return -1; }
     if (!make_map(&A.a[0], dg, T, F, F, kTileK) || !make_map(&A.a[1], du, T, F, F, kTileK) ||
-        !make_map(&A.b[0], x, T, D, ld_x, kTileK)) {
+        !make_map(&A.b[0], x, T, D, ld_x, kTileK) || (L.kind != kSingle && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";
       return -1;
     }
-    e = launch_gemm((const void*)gated_gemm_kernel<kDw>, A, sms, stream, "gated_ffn_bwd dw launch", why);
+    e = launch_gemm(L, A, stream, "gated_ffn_bwd dw launch", why);
     if (e) return e;
   }
   return 0;
