@@ -29,23 +29,14 @@ namespace {
 
 enum Mode { kGate, kDx, kDw };
 
-// Tile shapes (see the kernel): one CTA, 128 x tile_n; a pair of CTAs, 256 x 256
-// with two accumulators; a pair of CTAs, 512 x 256 in two accumulators.
-enum Kind { kSingle, kPair, kWide };
-
 constexpr int kTileK = 64;                       // contraction elements (128 bytes) per stage
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;                     // 4 lane quarters x 2 column halves
 constexpr int kThreads = 64 + 32 * kEpiWarps;    // producer warp, MMA warp, epilogue warps
 constexpr uint32_t kABytes = 128 * kTileK * 2;   // 128 rows of A
 constexpr uint32_t kTmemCols = 512;              // two accumulators of up to 256 columns
-constexpr uint32_t kBoxBytes = 32 * 128;         // a store box: 32 rows x 64 columns
+constexpr uint32_t kBoxBytes = 32 * 128;         // store box of an epilogue warp (pairs): 32 rows x 64 columns
 constexpr int kGroupM = 8;                       // tiles go m-first inside groups of 8 tile rows: operand reuse in L2
-
-// Store boxes an epilogue warp of a pair holds: h, gate and up; else one.
-__host__ __device__ constexpr int boxes(int mode, int kind) {
-  return kind == kSingle ? 0 : (mode == kGate ? 3 : 1);
-}
 
 struct Args {
   CUtensorMap a[2], b[2], c[3];                  // c: outputs, of pairs
@@ -54,9 +45,9 @@ struct Args {
   int64_t ld_out;
   int problems;
   int M, N;              // output rows and columns of one problem
-  int m_tiles, n_tiles;  // tiles of one problem (kWide: 512-row tiles that are whole 256-row halves)
-  int tiles, wide;       // work units of all problems; kWide: those that are whole 512-row tiles
-  int m_halves;          // kWide: 256-row halves of one problem
+  int m_tiles, n_tiles;  // tiles of one problem (pairs: whole 512-row tiles)
+  int tiles, whole;      // work units of all problems; pairs: those that are whole 512-row tiles
+  int m_halves;          // pairs: 256-row halves of one problem
   int n_k, n_k0;         // K stages of a tile, and of its first segment (kDx)
   int tile_n;            // output columns of a tile (kGate: features, each with a gate and an up column)
   int acc_n;             // accumulator columns: 2 * tile_n (kGate) or tile_n
@@ -174,8 +165,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Work unit t of the launch: problem, first output row, tile column, and for
-// kWide the 256-row halves it covers.
-// kWide: units of the last 256-row half when there is an odd number of them.
+// pairs the 256-row halves it covers.
+// Pairs: units of the last 256-row half when there is an odd number of them.
 __host__ __device__ __forceinline__ int odd_halves(const Args& A) {
   return A.m_halves & 1 ? A.problems * A.n_tiles : 0;
 }
@@ -196,16 +187,16 @@ __device__ __forceinline__ TilePos tile_of(const Args& A, int t, int rows) {
   q.halves = 2;
   return q;
 }
-template <int KIND>
+template <bool PAIR>
 __device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
-  if constexpr (KIND != kWide) return tile_of(A, t, KIND == kPair ? 256 : 128);
-  if (t < A.wide) return tile_of(A, t, 512);
+  if constexpr (!PAIR) return tile_of(A, t, 128);
+  if (t < A.whole) return tile_of(A, t, 512);
   // The tiles past the last full round, as halves; then the odd half row.
-  const int all = A.tiles == A.wide ? 0 : (A.tiles - A.wide - odd_halves(A)) / 2;
-  t -= A.wide;
+  const int all = A.tiles == A.whole ? 0 : (A.tiles - A.whole - odd_halves(A)) / 2;
+  t -= A.whole;
   TilePos q;
   if (t < 2 * all) {
-    q = tile_of(A, A.wide + t / 2, 512);
+    q = tile_of(A, A.whole + t / 2, 512);
     q.m0 += (t & 1) * 256;
   } else {
     t -= 2 * all;
@@ -254,28 +245,29 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 // range rows and columns arrive as zeros); warp 1 issues tcgen05.mma; warps
 // 2..9 drain the accumulators.  Every wait is bounded, as in gemm_mxfp8.cu.
 //
-// kSingle: one CTA, 128 rows x tile_n columns, two accumulators in turn, direct
-// stores -- few rows, where many narrow tiles stream the weights.
-// kPair: two CTAs (a cluster on two SMs) share a 256 x 256 tile.  Each loads its
-// 128 rows of A and half of B's 256 -- in kGate CTA 0 the gate rows and CTA 1
-// the up rows of the tile's 128 features, so both accumulators hold both --
-// and CTA 0 issues tcgen05.mma.cta_group::2 for the pair.  Two accumulators in
-// turn hide the epilogue, whose results leave through shared memory as 32 x 64
-// boxes by TMA: direct 16-byte stores of h, gate and up cost 180 of 1520 us at
-// 8192 x 4096 x 14336.
-// kWide: as kPair with 512 x 256 tiles: two M = 256 MMAs a K step on one B, a
-// quarter fewer operand bytes per product (the tensor cores wait for operands:
-// the 256 x 256 backward products ran 2766 us, 2346 with the copies left out).
-// Both accumulators fill at once, so a tile's epilogue is exposed except that
-// the next tile's first ring of stages goes to the first accumulator while the
-// second still drains; the contractions of the backward are long.  Tiles past
-// the last full round of pairs are dealt as 256-row halves.
+// Single CTAs: tiles of 128 rows x tile_n columns, two accumulators in turn,
+// direct stores -- few rows, where many narrow tiles stream the weights.
+// PAIR: two CTAs (a cluster on two SMs) share tiles of 512 x 256, in two M = 256
+// accumulators on one B.  Each CTA loads its 128 rows of either 256-row half of
+// A and half of B's 256 -- in kGate CTA 0 the gate rows and CTA 1 the up rows of
+// the tile's 128 features, so both accumulators hold both -- and CTA 0 issues
+// tcgen05.mma.cta_group::2 for the pair.  What bounds this is the operand
+// stream from L2: with 256 x 256 tiles and two accumulators in turn the tensor
+// cores were busy 68% of 1456 us forward (8192 x 4096 x 14336, gate and up
+// kept), 512 x 256 moves a quarter fewer operand bytes per product and runs
+// 1301 us forward (1228 without keeping them) and 1237 and 1257 us for the two
+// products of the backward, 93% busy; copies left out, the same MMAs take 1205.
+// Both accumulators fill at once, so a tile's epilogue is exposed, but for
+// this: the next tile's first ring of stages goes to the first accumulator
+// while the second still drains, and accumulators go back before the stores.
+// Results leave through shared memory as 32 x 64 boxes by TMA (direct 16-byte
+// stores cost 180 us of the forward).  Tiles past the last full round of pairs
+// are dealt as 256-row halves.
 // Copies of both CTAs of a pair complete on CTA 0's barriers, one
 // tcgen05.commit per CTA frees the stages, and no copy is multicast.
-template <int MODE, int KIND>
+template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_constant__ Args A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  constexpr bool PAIR = KIND != kSingle;
   if constexpr (PAIR) {
     // Without a two-CTA cluster the paired allocation would wait for a partner that does not exist.
     if (cluster_size() != 2) {
@@ -286,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
   const int first = PAIR ? (int)cluster_id_x() : (int)blockIdx.x, step = PAIR ? (int)n_clusters_x() : (int)gridDim.x;
   uint8_t* store_box = smem_raw + (size_t)A.stages * A.stage_bytes;
-  Barriers& S = *reinterpret_cast<Barriers*>(store_box + (size_t)kEpiWarps * boxes(MODE, KIND) * kBoxBytes);
+  Barriers& S = *reinterpret_cast<Barriers*>(store_box + (PAIR ? (size_t)kEpiWarps * kBoxBytes : 0));
   constexpr bool kAmn = MODE == kDw, kBmn = MODE != kGate;
-  constexpr uint32_t kAHalf = kABytes;           // kWide: a stage holds two 128-row blocks of A, then B
+  constexpr uint32_t kBOff = PAIR ? 2 * kABytes : kABytes;           // of a stage: one or two blocks of A, then B
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -321,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
       uint32_t s = 0, ph = 1;
       bool ok = true;
       for (int t = first; t < A.tiles && ok; t += step) {
-        const TilePos q = tile_pos<KIND>(A, t);
-        // bytes of a stage: kWide tiles of one half leave A's second block out
-        const uint32_t bytes = KIND == kWide && q.halves == 1 ? A.stage_bytes - kAHalf : A.stage_bytes;
+        const TilePos q = tile_pos<PAIR>(A, t);
+        // bytes of a stage: tiles of one half leave A's second block out
+        const uint32_t bytes = PAIR && q.halves == 1 ? A.stage_bytes - kABytes : A.stage_bytes;
         for (int kb = 0; kb < A.n_k; ++kb) {
           if (!mbar_wait_bounded(&S.empty[s], ph, A.status) || failed_flag(S)) {
             atomicOr(&S.failed, 1u);
@@ -331,12 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             break;
           }
           uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes;
-          uint8_t* sb = sa + (KIND == kWide ? 2 * kAHalf : kABytes);
+          uint8_t* sb = sa + kBOff;
           const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
           if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * bytes : bytes);
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) { tma_load<PAIR>(dst, map, x, y, bar); };
+          const int blocks = PAIR ? q.halves : 1;
           if constexpr (MODE == kGate) {
-            load(sa, &A.a[0], kb * kTileK, q.m0 + (int)rank * 128);
+            for (int h = 0; h < blocks; ++h) load(sa + h * kABytes, &A.a[0], kb * kTileK, q.m0 + h * 256 + (int)rank * 128);
             if constexpr (PAIR) {
               load(sb, &A.b[rank], kb * kTileK, q.nt * A.tile_n);
             } else {
@@ -345,15 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             }
           } else {
             const int n0 = q.nt * A.tile_n + (PAIR ? (int)rank * 128 : 0), nb = PAIR ? 128 : A.tile_n;
-            const int blocks = KIND == kWide ? q.halves : 1;
             const int seg = MODE == kDx && kb >= A.n_k0, k0 = (kb - seg * A.n_k0) * kTileK;
             for (int h = 0; h < blocks; ++h) {
               const int m = q.m0 + h * 256 + (int)rank * 128;
               if constexpr (MODE == kDx) {
-                load(sa + h * kAHalf, &A.a[seg], k0, m);
+                load(sa + h * kABytes, &A.a[seg], k0, m);
               } else {
-                load(sa + h * kAHalf, &A.a[q.p], m, k0);
-                load(sa + h * kAHalf + kAHalf / 2, &A.a[q.p], m + 64, k0);
+                load(sa + h * kABytes, &A.a[q.p], m, k0);
+                load(sa + h * kABytes + kABytes / 2, &A.a[q.p], m + 64, k0);
               }
             }
             for (int c = 0; c < nb; c += 64) load(sb + c * 128, &A.b[seg], n0 + c, k0);
@@ -386,14 +378,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
       };
       // One stage into accumulator `acc`, from the h-th block of A.
       auto mma_stage = [&](uint32_t stage, int h, uint32_t acc, bool first_k) {
-        const uint32_t a0 = smem_u32(smem_raw) + stage * A.stage_bytes + (uint32_t)h * kAHalf;
-        const uint32_t b0 = smem_u32(smem_raw) + stage * A.stage_bytes + (KIND == kWide ? 2 * kAHalf : kABytes);
+        const uint32_t a0 = smem_u32(smem_raw) + stage * A.stage_bytes + (uint32_t)h * kABytes;
+        const uint32_t b0 = smem_u32(smem_raw) + stage * A.stage_bytes + kBOff;
 #pragma unroll
         for (int k = 0; k < kTileK / 16; ++k)
           mma_bf16<PAIR>(tmem + acc * 256u, op_desc(a0, k, kAmn), op_desc(b0, k, kBmn), idesc, (!first_k || k > 0) ? 1u : 0u);
       };
       for (int t = first; t < A.tiles && ok; t += step, ++it) {
-        if constexpr (KIND != kWide) {
+        if constexpr (!PAIR) {
           const uint32_t acc = it & 1u;
           wait(&S.acc_empty[acc], (uses[acc]++ & 1u) ^ 1u);
           for (int kb = 0; kb < A.n_k && ok; ++kb) {
@@ -405,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           }
           if (ok) commit(&S.acc_full[acc]);
         } else {
-          const int halves = tile_pos<KIND>(A, t).halves;
+          const int halves = tile_pos<PAIR>(A, t).halves;
           const int lead = halves == 2 ? min(A.n_k, A.stages) : 0;   // stages that go to the first accumulator alone
           wait(&S.acc_empty[0], (uses[0]++ & 1u) ^ 1u);
           uint32_t s1 = s;
@@ -446,17 +438,28 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;                // tcgen05.ld reaches lanes 32 * (warp % 4) ..
     const int half = (warp - 2) >> 2;
-    uint8_t* box = store_box + (size_t)(warp - 2) * boxes(MODE, KIND) * kBoxBytes;
-    // 8 columns (16 bytes) of this lane's row in a store box: 128-byte swizzle
-    auto put = [&](int b, int col8, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-      sts128(smem_u32(box) + (uint32_t)b * kBoxBytes + 128u * lane + 16u * (col8 ^ (lane & 7)), make_uint4(x, y, z, w));
+    uint8_t* box = store_box + (size_t)(warp - 2) * kBoxBytes;
+    // 16 columns (32 bytes) of this lane's row to the store box: 128-byte swizzle
+    auto put2 = [&](int col8, const uint32_t (&o)[8]) {
+      const uint32_t at = smem_u32(box) + 128u * lane;
+      sts128(at + 16u * (col8 ^ (lane & 7)), make_uint4(o[0], o[1], o[2], o[3]));
+      sts128(at + 16u * ((col8 + 1) ^ (lane & 7)), make_uint4(o[4], o[5], o[6], o[7]));
+    };
+    // The MMA thread may overwrite the accumulator.
+    auto hand_back = [&](uint32_t acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&S.acc_empty[acc]);
+        else mbar_arrive_remote(cluster_addr(&S.acc_empty[acc], 0));
+      }
     };
     uint32_t it = 0, uses[2] = {0, 0};
     bool ok = true;
     for (int t = first; t < A.tiles && ok; t += step, ++it) {
-      const TilePos q = tile_pos<KIND>(A, t);
-      for (int a = 0; a < (KIND == kWide ? q.halves : 1) && ok; ++a) {
-        const uint32_t acc = KIND == kWide ? (uint32_t)a : (it & 1u);
+      const TilePos q = tile_pos<PAIR>(A, t);
+      for (int a = 0; a < (PAIR ? q.halves : 1) && ok; ++a) {
+        const uint32_t acc = PAIR ? (uint32_t)a : (it & 1u);
         const bool got = mbar_wait_bounded(&S.acc_full[acc], uses[acc]++ & 1u, A.status);
         tc_fence_after();
         if (!got || failed_flag(S)) {
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
         }
         const int row0 = q.m0 + a * 256 + (int)rank * 128 + quarter * 32;
         const uint32_t ta = tmem + acc * 256u + ((uint32_t)(quarter * 32) << 16);
-        if constexpr (KIND == kSingle) {
+        if constexpr (!PAIR) {
           const int row = row0 + lane;
           const bool live = row < A.M;
           for (int c = half * 16; c < A.tile_n; c += 32) {
@@ -496,36 +499,37 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             __syncwarp();                        // tcgen05.ld needs the warp converged
           }
         } else if constexpr (MODE == kGate) {
-          // 64 features a warp: h, and gate and up when kept
+          // 64 features a warp: h, and gate and up when kept, packed in
+          // registers so that the accumulator goes back before the stores
           const int col0 = q.nt * A.tile_n + half * 64;
-          const bool keep = A.out[1] != nullptr;
-          if (lane == 0) bulk_wait_read_all();   // the boxes of the tile before have left
-          __syncwarp();
+          uint32_t o[3][4][8];
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            uint32_t r[16], u[16], o[8];
-            tmem_ld16(ta + (uint32_t)(half * 64 + c), r);
-            tmem_ld16(ta + (uint32_t)(128 + half * 64 + c), u);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[16], u[16];
+            tmem_ld16(ta + (uint32_t)(half * 64 + 16 * c), r);
+            tmem_ld16(ta + (uint32_t)(128 + half * 64 + 16 * c), u);
             tmem_ld16_fence(r, true);
             tmem_ld16_fence(u, false);
-            gate_product(A.act, r, u, o);
-            put(0, c / 8, o[0], o[1], o[2], o[3]);
-            put(0, c / 8 + 1, o[4], o[5], o[6], o[7]);
-            if (keep) {
-              pack16(r, o);
-              put(1, c / 8, o[0], o[1], o[2], o[3]);
-              put(1, c / 8 + 1, o[4], o[5], o[6], o[7]);
-              pack16(u, o);
-              put(2, c / 8, o[0], o[1], o[2], o[3]);
-              put(2, c / 8 + 1, o[4], o[5], o[6], o[7]);
-            }
+            gate_product(A.act, r, u, o[0][c]);
+            pack16(r, o[1][c]);
+            pack16(u, o[2][c]);
             __syncwarp();
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && row0 < A.M && col0 < A.N) {
-            for (int b = 0; b < (keep ? 3 : 1); ++b) tma_store_2d(&A.c[b], box + b * kBoxBytes, col0, row0);
-            bulk_commit();
+          hand_back(acc);
+          const int n_out = A.out[1] ? 3 : 1;
+#pragma unroll
+          for (int b = 0; b < 3; ++b) {
+            if (b >= n_out) break;
+            if (lane == 0) bulk_wait_read_all();   // the box before has left
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) put2(2 * c, o[b][c]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < A.M && col0 < A.N) {
+              tma_store_2d(&A.c[b], box, col0, row0);
+              bulk_commit();
+            }
           }
         } else {
           // 128 columns a warp, in two boxes through one buffer
@@ -543,8 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               pack16(r[c], o);
-              put(0, 2 * c, o[0], o[1], o[2], o[3]);
-              put(0, 2 * c + 1, o[4], o[5], o[6], o[7]);
+              put2(2 * c, o);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -554,12 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {                         // the MMA thread may overwrite this accumulator
-          if (rank == 0) mbar_arrive(&S.acc_empty[acc]);
-          else mbar_arrive_remote(cluster_addr(&S.acc_empty[acc], 0));
-        }
+        if constexpr (!(PAIR && MODE == kGate)) hand_back(acc);
       }
     }
     if (PAIR && lane == 0) bulk_wait_read_all(); // before the CTA's shared memory goes
@@ -682,23 +680,23 @@ int pair_capacity(const void* kernel, int mode, size_t smem) {
 
 struct Launch {
   const void* kernel;
-  int kind, grid;
+  bool pair;
+  int grid;
   size_t smem;
 };
 
-const void* kernel_of(int mode, int kind) {
-  if (mode == kGate)
-    return kind == kSingle ? (const void*)gated_gemm_kernel<kGate, kSingle> : (const void*)gated_gemm_kernel<kGate, kPair>;
-  if (mode == kDx)
-    return kind == kSingle ? (const void*)gated_gemm_kernel<kDx, kSingle> : (const void*)gated_gemm_kernel<kDx, kWide>;
-  return kind == kSingle ? (const void*)gated_gemm_kernel<kDw, kSingle> : (const void*)gated_gemm_kernel<kDw, kWide>;
+template <int MODE>
+const void* kernel_of(bool pair) {
+  return pair ? (const void*)gated_gemm_kernel<MODE, true> : (const void*)gated_gemm_kernel<MODE, false>;
+}
+const void* kernel_of(int mode, bool pair) {
+  return mode == kGate ? kernel_of<kGate>(pair) : mode == kDx ? kernel_of<kDx>(pair) : kernel_of<kDw>(pair);
 }
 
 // Fills the tile and ring geometry of a launch.  Returns false when the tiles
 // outnumber an int.
 bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   const int unit = mode == kGate ? 16 : 64, widest = mode == kGate ? 128 : 256;
-  const int wide_kind = mode == kGate ? kPair : kWide;
   A.problems = problems;
   // Single CTAs: the tile width that divides the columns over the SMs in the
   // fewest rounds of equal cost; a tile costs its columns, and its 128 rows of
@@ -712,56 +710,55 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
       A.tile_n = w;
     }
   }
-  L->kind = kSingle;
+  L->pair = false;
   // Pairs.
-  const uint32_t pair_stage = (wide_kind == kWide ? 3 : 2) * kABytes;
-  const size_t pair_boxes = (size_t)kEpiWarps * boxes(mode, wide_kind) * kBoxBytes;
-  const int pair_stages = (int)((kSmemCap - pair_boxes) / pair_stage);
-  const size_t pair_smem = (size_t)pair_stages * pair_stage + pair_boxes + sizeof(Barriers);
+  constexpr uint32_t kPairStage = 3 * kABytes;
+  constexpr int kPairStages = (int)((kSmemCap - kEpiWarps * kBoxBytes) / kPairStage);
+  constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + kEpiWarps * kBoxBytes + sizeof(Barriers);
   int pairs = 0;
   if (A.M > 128) {
-    pairs = pair_capacity(kernel_of(mode, wide_kind), mode, pair_smem);
+    pairs = pair_capacity(kernel_of(mode, true), mode, kPairSmem);
     if (pairs > sms / 2) pairs = sms / 2;
     const int64_t tiles = (int64_t)cdiv(A.M, 256) * cdiv(A.N, widest) * problems;
     const int64_t cost = pairs ? ((tiles + pairs - 1) / pairs) * 256 : best;
     if (cost < best) {
-      L->kind = wide_kind;
+      L->pair = true;
       A.tile_n = widest;
     }
   }
   A.n_tiles = cdiv(A.N, A.tile_n);
-  A.m_tiles = cdiv(A.M, L->kind == kSingle ? 128 : 256);
-  A.m_halves = A.m_tiles;
+  A.m_tiles = cdiv(A.M, L->pair ? 256 : 128);
   int64_t tiles = (int64_t)A.m_tiles * A.n_tiles * problems;
   if (tiles > 0x7FFFFFFF - sms) return false;
-  int units = L->kind == kSingle ? sms : pairs;
-  if (L->kind == kWide) {
+  if (L->pair) {
+    A.m_halves = A.m_tiles;
     A.m_tiles = A.m_halves / 2;
-    const int64_t whole = (int64_t)A.m_tiles * A.n_tiles * problems, odd = (A.m_halves & 1) * A.n_tiles * (int64_t)problems;
+    const int64_t whole = (int64_t)A.m_tiles * A.n_tiles * problems, odd = odd_halves(A);
     const int64_t rest = whole % pairs;          // past the last full round
-    A.wide = (int)(2 * rest + odd <= pairs ? whole - rest : whole);
-    tiles = A.wide + 2 * (whole - A.wide) + odd;
+    A.whole = (int)(2 * rest + odd <= pairs ? whole - rest : whole);
+    tiles = A.whole + 2 * (whole - A.whole) + odd;
   }
   A.tiles = (int)tiles;
   A.acc_n = mode == kGate ? 2 * A.tile_n : A.tile_n;
-  if (L->kind == kSingle) {
+  if (L->pair) {
+    A.stage_bytes = kPairStage;
+    A.stages = kPairStages;
+    L->smem = kPairSmem;
+    L->grid = 2 * (A.tiles < pairs ? A.tiles : pairs);
+  } else {
     A.stage_bytes = kABytes + (uint32_t)A.acc_n * 128u;
     A.stages = (int)(kSmemCap / A.stage_bytes);
     if (A.stages > kMaxStages) A.stages = kMaxStages;
     L->smem = (size_t)A.stages * A.stage_bytes + sizeof(Barriers);
-  } else {
-    A.stage_bytes = pair_stage;
-    A.stages = pair_stages;
-    L->smem = pair_smem;
+    L->grid = A.tiles < sms ? A.tiles : sms;
   }
-  L->kernel = kernel_of(mode, L->kind);
-  L->grid = (A.tiles < units ? A.tiles : units) * (L->kind == kSingle ? 1 : 2);
+  L->kernel = kernel_of(mode, L->pair);
   return true;
 }
 
 int launch_gemm(const Launch& L, Args& A, cudaStream_t stream, const char* what, const char** why) {
   void* argv[] = {&A};
-  return launch_pdl(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.kind != kSingle);
+  return launch_pdl(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.pair);
 }
 
 // Maps of the outputs (bf16 [rows, cols] dense) for store boxes.
@@ -789,7 +786,7 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
   Launch L;
   if (!plan_tiles(A, kGate, 1, sms, &L)) { *why = "too many tiles"; return -1; }
   if (!make_map(&A.a[0], x, T, D, ld_x, 128) || !make_map(&A.b[0], w_gate, F, D, ld_w, A.tile_n) ||
-      !make_map(&A.b[1], w_up, F, D, ld_w, A.tile_n) || (L.kind != kSingle && !make_out_maps(A))) {
+      !make_map(&A.b[1], w_up, F, D, ld_w, A.tile_n) || (L.pair && !make_out_maps(A))) {
     *why = "cuTensorMapEncodeTiled failed";
     return -1;
   }
@@ -824,7 +821,7 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     if (!plan_tiles(A, kDx, 1, sms, &L)) { *why = "too many tiles"; return -1; }
     if (!make_map(&A.a[0], dg, T, F, F, 128) || !make_map(&A.a[1], du, T, F, F, 128) ||
         !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK) ||
-        (L.kind != kSingle && !make_out_maps(A))) {
+        (L.pair && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";
       return -1;
     }
@@ -843,7 +840,7 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     Launch L;
     if (!plan_tiles(A, kDw, 2, sms, &L)) { *why = "too many tiles"; return -1; }
     if (!make_map(&A.a[0], dg, T, F, F, kTileK) || !make_map(&A.a[1], du, T, F, F, kTileK) ||
-        !make_map(&A.b[0], x, T, D, ld_x, kTileK) || (L.kind != kSingle && !make_out_maps(A))) {
+        !make_map(&A.b[0], x, T, D, ld_x, kTileK) || (L.pair && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";
       return -1;
     }
