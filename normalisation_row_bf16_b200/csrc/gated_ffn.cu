@@ -52,6 +52,7 @@ struct Args {
   int tile_n;            // output columns of a tile (kGate: features, each with a gate and an up column)
   int acc_n;             // accumulator columns: 2 * tile_n (kGate) or tile_n
   int act;
+  int a_rows;            // rows of A that a stage of a single CTA holds
   int stages;
   uint32_t stage_bytes;
 };
@@ -87,40 +88,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// 2-D tensor copy into this CTA's shared memory, completing on the barrier at
-// shared::cluster address `bar` (of a pair, CTA 0's).
-template <bool PAIR>
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (PAIR)
-    tma_load_2d_pair(dst, map, x, y, bar);
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// All 512 columns of tensor memory, by one warp (of each CTA of a pair).
-template <bool PAIR>
-__device__ __forceinline__ void tmem_alloc(uint32_t* base) {
-  if constexpr (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(base)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(base)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-}
-template <bool PAIR>
-__device__ __forceinline__ void tmem_free(uint32_t tmem) {
-  if constexpr (PAIR)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
-  else
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator (bit 4), A and B bf16
@@ -208,7 +175,7 @@ __device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
   return q;
 }
 
-// 16 output columns of one row, from col on: N is a multiple of 8.
+// 16 output columns of one row, from col on, those below n (a multiple of 8).
 __device__ __forceinline__ void store_cols16(uint16_t* row, int col, int n, const uint32_t (&o)[8]) {
   if (col < n) *reinterpret_cast<uint4*>(row + col) = make_uint4(o[0], o[1], o[2], o[3]);
   if (col + 8 < n) *reinterpret_cast<uint4*>(row + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -246,7 +213,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 // 2..9 drain the accumulators.  Every wait is bounded, as in gemm_mxfp8.cu.
 //
 // Single CTAs: tiles of 128 rows x tile_n columns, two accumulators in turn,
-// direct stores -- few rows, where many narrow tiles stream the weights.
+// direct stores -- few rows, where many narrow tiles stream the weights.  Below
+// 128 rows a stage holds only the rows of A there are (in eights), so that more
+// stages of weights are in flight; the MMA's 128-row window runs on into the
+// bytes behind them, which only reach accumulator rows that are never stored.
 // PAIR: two CTAs (a cluster on two SMs) share tiles of 512 x 256, in two M = 256
 // accumulators on one B.  Each CTA loads its 128 rows of either 256-row half of
 // A and half of B's 256 -- in kGate CTA 0 the gate rows and CTA 1 the up rows of
@@ -280,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
   uint8_t* store_box = smem_raw + (size_t)A.stages * A.stage_bytes;
   Barriers& S = *reinterpret_cast<Barriers*>(store_box + (PAIR ? (size_t)kEpiWarps * kBoxBytes : 0));
   constexpr bool kAmn = MODE == kDw, kBmn = MODE != kGate;
-  constexpr uint32_t kBOff = PAIR ? 2 * kABytes : kABytes;           // of a stage: one or two blocks of A, then B
+  const uint32_t b_off = PAIR ? 2 * kABytes : (uint32_t)A.a_rows * 128u;   // of a stage: A, then B
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -297,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
     fence_barrier_init();
   }
   __syncwarp();
-  if (warp == 0) tmem_alloc<PAIR>(&S.tmem_base);
+  if (warp == 0) tmem_alloc<PAIR>(&S.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();        // both CTAs' barriers and allocation are in place
@@ -323,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             break;
           }
           uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes;
-          uint8_t* sb = sa + kBOff;
+          uint8_t* sb = sa + b_off;
           const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
           if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * bytes : bytes);
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) { tma_load<PAIR>(dst, map, x, y, bar); };
@@ -379,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
       // One stage into accumulator `acc`, from the h-th block of A.
       auto mma_stage = [&](uint32_t stage, int h, uint32_t acc, bool first_k) {
         const uint32_t a0 = smem_u32(smem_raw) + stage * A.stage_bytes + (uint32_t)h * kABytes;
-        const uint32_t b0 = smem_u32(smem_raw) + stage * A.stage_bytes + kBOff;
+        const uint32_t b0 = smem_u32(smem_raw) + stage * A.stage_bytes + b_off;
 #pragma unroll
         for (int k = 0; k < kTileK / 16; ++k)
           mma_bf16<PAIR>(tmem + acc * 256u, op_desc(a0, k, kAmn), op_desc(b0, k, kBmn), idesc, (!first_k || k > 0) ? 1u : 0u);
@@ -472,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
         if constexpr (!PAIR) {
           const int row = row0 + lane;
           const bool live = row < A.M;
+          const int end = min(A.N, (q.nt + 1) * A.tile_n);
           for (int c = half * 16; c < A.tile_n; c += 32) {
             const int col = q.nt * A.tile_n + c;
             uint32_t r[16], o[8];
@@ -483,18 +454,18 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
               tmem_ld16_fence(u, false);
               gate_product(A.act, r, u, o);
               if (live) {
-                store_cols16(A.out[0] + (int64_t)row * A.ld_out, col, A.N, o);
+                store_cols16(A.out[0] + (int64_t)row * A.ld_out, col, end, o);
                 if (A.out[1]) {
                   pack16(r, o);
-                  store_cols16(A.out[1] + (int64_t)row * A.ld_out, col, A.N, o);
+                  store_cols16(A.out[1] + (int64_t)row * A.ld_out, col, end, o);
                   pack16(u, o);
-                  store_cols16(A.out[2] + (int64_t)row * A.ld_out, col, A.N, o);
+                  store_cols16(A.out[2] + (int64_t)row * A.ld_out, col, end, o);
                 }
               }
             } else {
               tmem_ld16_fence(r, true);
               pack16(r, o);
-              if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, A.N, o);
+              if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, end, o);
             }
             __syncwarp();                        // tcgen05.ld needs the warp converged
           }
@@ -577,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();        // no MMA, copy or remote arrive into either CTA remains
   tc_fence_after();
-  if (warp == 0) tmem_free<PAIR>(tmem);
+  if (warp == 0) tmem_free<PAIR>(tmem, kTmemCols);
 }
 
 // dg = dh * up * act'(gate), du = dh * act(gate): 8 elements a thread and step.
@@ -649,35 +620,6 @@ int launch_pdl(const void* kernel, int grid, int threads, size_t smem, void** ar
   return 0;
 }
 
-// Pairs of CTAs of a kernel that fit on the device at once (0 if none), looked
-// up once per device and kernel.
-int pair_capacity(const void* kernel, int mode, size_t smem) {
-  static std::mutex mu;
-  static int cached[64][3];                      // pairs + 1
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::lock_guard<std::mutex> lk(mu);
-  if (cached[dev][mode]) return cached[dev][mode] - 1;
-  int n = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
-  }
-  cudaGetLastError();
-  cached[dev][mode] = n + 1;
-  return n;
-}
-
 struct Launch {
   const void* kernel;
   bool pair;
@@ -696,15 +638,16 @@ const void* kernel_of(int mode, bool pair) {
 // Fills the tile and ring geometry of a launch.  Returns false when the tiles
 // outnumber an int.
 bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
-  const int unit = mode == kGate ? 16 : 64, widest = mode == kGate ? 128 : 256;
+  const int unit = mode == kGate ? 8 : 64, widest = mode == kGate ? 128 : 256;
   A.problems = problems;
   // Single CTAs: the tile width that divides the columns over the SMs in the
-  // fewest rounds of equal cost; a tile costs its columns, and its 128 rows of
-  // A once more.
+  // fewest rounds of equal cost; a tile costs its columns, and its rows of A
+  // half as much (they come from L2).
+  A.a_rows = mode == kDw || A.M >= 128 ? 128 : (A.M + 7) / 8 * 8;
   int64_t best = 0;
   for (int w = widest; w >= unit; w -= unit) {
     const int64_t tiles = (int64_t)cdiv(A.M, 128) * cdiv(A.N, w) * problems;
-    const int64_t cost = ((tiles + sms - 1) / sms) * ((mode == kGate ? 2 * w : w) + 64);
+    const int64_t cost = ((tiles + sms - 1) / sms) * ((mode == kGate ? 2 * w : w) + A.a_rows / 2);
     if (best == 0 || cost < best) {
       best = cost;
       A.tile_n = w;
@@ -717,7 +660,7 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + kEpiWarps * kBoxBytes + sizeof(Barriers);
   int pairs = 0;
   if (A.M > 128) {
-    pairs = pair_capacity(kernel_of(mode, true), mode, kPairSmem);
+    pairs = cta_pair_capacity(kernel_of(mode, true), kThreads, kPairSmem, mode);
     if (pairs > sms / 2) pairs = sms / 2;
     const int64_t tiles = (int64_t)cdiv(A.M, 256) * cdiv(A.N, widest) * problems;
     const int64_t cost = pairs ? ((tiles + pairs - 1) / pairs) * 256 : best;
@@ -746,10 +689,12 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
     L->smem = kPairSmem;
     L->grid = 2 * (A.tiles < pairs ? A.tiles : pairs);
   } else {
-    A.stage_bytes = kABytes + (uint32_t)A.acc_n * 128u;
+    A.stage_bytes = (uint32_t)(A.a_rows + A.acc_n) * 128u;
     A.stages = (int)(kSmemCap / A.stage_bytes);
     if (A.stages > kMaxStages) A.stages = kMaxStages;
     L->smem = (size_t)A.stages * A.stage_bytes + sizeof(Barriers);
+    const size_t window = (size_t)(A.stages - 1) * A.stage_bytes + kABytes;    // the last stage's 128 rows of A
+    if (L->smem < window) L->smem = window;
     L->grid = A.tiles < sms ? A.tiles : sms;
   }
   L->kernel = kernel_of(mode, L->pair);
@@ -770,6 +715,33 @@ bool make_out_maps(Args& A) {
 
 }  // namespace
 
+int cta_pair_capacity(const void* kernel, int threads, size_t smem, int slot) {
+  static std::mutex mu;
+  static int cached[64][4];                      // pairs + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || slot < 0 || slot >= 4) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  if (cached[dev][slot]) return cached[dev][slot] - 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  cached[dev][slot] = n + 1;
+  return n;
+}
+
 int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up, int T,
                          int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
                          cudaStream_t stream, const char** why) {
@@ -785,7 +757,7 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
   A.n_k = A.n_k0 = cdiv(D, kTileK);
   Launch L;
   if (!plan_tiles(A, kGate, 1, sms, &L)) { *why = "too many tiles"; return -1; }
-  if (!make_map(&A.a[0], x, T, D, ld_x, 128) || !make_map(&A.b[0], w_gate, F, D, ld_w, A.tile_n) ||
+  if (!make_map(&A.a[0], x, T, D, ld_x, A.a_rows) || !make_map(&A.b[0], w_gate, F, D, ld_w, A.tile_n) ||
       !make_map(&A.b[1], w_up, F, D, ld_w, A.tile_n) || (L.pair && !make_out_maps(A))) {
     *why = "cuTensorMapEncodeTiled failed";
     return -1;
@@ -819,7 +791,7 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     A.n_k = 2 * A.n_k0;
     Launch L;
     if (!plan_tiles(A, kDx, 1, sms, &L)) { *why = "too many tiles"; return -1; }
-    if (!make_map(&A.a[0], dg, T, F, F, 128) || !make_map(&A.a[1], du, T, F, F, 128) ||
+    if (!make_map(&A.a[0], dg, T, F, F, A.a_rows) || !make_map(&A.a[1], du, T, F, F, A.a_rows) ||
         !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK) ||
         (L.pair && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";

@@ -7,11 +7,10 @@
 // scales, the operand of the next product -- so the fp32 result is rounded
 // once either way and never makes a trip through memory in between.
 //
-// The kernel is the 128 x 256 tile of gemm_mxfp8.cu with the tile's 256
-// columns made of 128 gate and the same 128 up features (each a whole 128-row
-// scale atom).  A lane of the epilogue holds one row's gate and up values of
-// the same 32 features, one MX block of h: activation, product, block maximum,
-// scale and codes need no exchange between threads.
+// Tiles hold 128 gate and the same 128 up features (each a whole 128-row scale
+// atom) in 256 accumulator columns.  A lane of the epilogue holds one row's
+// gate and up values of the same 32 features, one MX block of h: activation,
+// product, block maximum, scale and codes need no exchange between threads.
 #include "gated_mxfp8.h"
 
 #include "activations.cuh"
@@ -21,46 +20,45 @@
 namespace mxn {
 namespace {
 
-constexpr int kTileM = 128, kTileF = 128, kTileK = 128;
-constexpr int kStages = 4;
+constexpr int kTileF = 128, kTileK = 128;        // features of a tile; K elements (= bytes) per stage
+constexpr int kMaxStages = 8;
 constexpr int kEpiWarps = 8;                     // 4 lane quarters x 2 feature halves
 constexpr int kThreads = 64 + 32 * kEpiWarps;    // producer warp, MMA warp, epilogue warps
-constexpr uint32_t kABytes = kTileM * kTileK;
-constexpr uint32_t kBBytes = 2 * kTileF * kTileK;
+constexpr uint32_t kRows128 = 128 * kTileK;      // 128 rows of an operand
 constexpr uint32_t kAtom = 512;                  // one 128 x 4 scale atom
-constexpr uint32_t kStageTx = kABytes + kBBytes + 3 * kAtom;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol0 = 256;                // accumulator: columns 0..255; scales: 12 per stage
 constexpr int kGroupM = 8;                       // tiles go m-first inside groups of 8 tile rows
 
-struct Smem {
-  uint8_t a[kStages][kABytes];                   // 1024-aligned (128B swizzle atoms)
-  uint8_t b[kStages][kBBytes];                   // 128 gate rows, 128 up rows
-  uint8_t sf[kStages][3 * kAtom];                // A, gate, up
-  uint64_t full[kStages], empty[kStages];
+struct Args {
+  CUtensorMap a, w[2];                           // codes: A, gate and up
+  CUtensorMap a_sf, w_sf[2];                     // pairs: their scale atoms as boxes of 4 rows of 128 bytes
+  const uint8_t *a_s, *w_s[2];
+  uint8_t *h, *h_s;
+  unsigned* status;
+  int T, F, K, m_tiles, n_tiles, act;
+  int out;                                       // 0 bf16; 1 E4M3, scales row-major; 2 E4M3, scales in the tcgen05 layout
+  int a_rows, stages;                            // rows of A a stage holds (single CTAs), ring depth
+  uint32_t sf_off, stage_bytes;                  // of a stage: B after A's rows, scales at sf_off
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t acc_full, acc_empty, mma_done;
   uint32_t tmem_base;
   uint32_t failed;
 };
 
-struct Args {
-  CUtensorMap a, g, u;
-  const uint8_t *a_s, *g_s, *u_s;
-  uint8_t *h, *h_s;
-  unsigned* status;
-  int T, F, K, m_tiles, n_tiles, act;
-  int out;                                       // 0 bf16; 1 E4M3, scales row-major; 2 E4M3, scales in the tcgen05 layout
-};
-
-__device__ __forceinline__ bool failed_flag(const Smem& S) {
+__device__ __forceinline__ bool failed_flag(const Barriers& S) {
   return *reinterpret_cast<const volatile uint32_t*>(&S.failed) != 0;
 }
 
-// As in gemm_mxfp8.cu: E4M3 operands, E8M0 scales, M = 128, N = 256, K = 32.
-__device__ __forceinline__ uint32_t instr_desc(uint32_t sf_id) {
-  return (sf_id << 4) | ((uint32_t)(256 >> 3) << 17) | (1u << 23) | ((uint32_t)(kTileM >> 4) << 24) | (sf_id << 29);
+// As in gemm_mxfp8.cu: E4M3 operands, E8M0 scales, M = m, N = 256, K = 32.
+__device__ __forceinline__ uint32_t instr_desc(uint32_t m, uint32_t sf_id) {
+  return (sf_id << 4) | ((uint32_t)(256 >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | (sf_id << 29);
 }
 
+// Tile t: 128-row (pairs: 256-row) block and feature block.
 __device__ __forceinline__ void tile_pos(const Args& A, int t, int* mt, int* nt) {
   const int m0 = t / (kGroupM * A.n_tiles) * kGroupM;
   const int gm = min(kGroupM, A.m_tiles - m0);
@@ -119,33 +117,49 @@ __device__ __forceinline__ void store_mxfp8(const Args& A, int row, int col, con
   A.h_s[at] = (uint8_t)(bad ? 0xFF : e + 127);
 }
 
+// Persistent CTAs as in gemm_mxfp8.cu.  PAIR: two CTAs (a cluster on two SMs)
+// share 256 x 256 tiles; each loads 128 rows of A with their scale atom, one of
+// the two weights' 128 rows (CTA 0 gate, CTA 1 up) and both weights' atoms, and
+// CTA 0 issues tcgen05.mma.cta_group::2 for both: a third fewer operand bytes
+// from L2, which bound the 128 x 256 tiles (11.4 GB in 855 us at 8192 x 14336 x
+// 4096).  Single CTAs take the calls of few rows: a stage then holds only the
+// rows of A there are (in eights), so that more stages of weights are in
+// flight; the MMA's 128-row window runs on into the bytes behind them, which
+// only reach accumulator rows that are never stored.
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_constant__ Args A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+  if constexpr (PAIR) {
+    // Without a two-CTA cluster the paired allocation would wait for a partner that does not exist.
+    if (cluster_size() != 2) {
+      if (threadIdx.x == 0) atomicOr(A.status, kStatusWaitTimeout);
+      return;
+    }
+  }
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int first = PAIR ? (int)cluster_id_x() : (int)blockIdx.x, step = PAIR ? (int)n_clusters_x() : (int)gridDim.x;
+  Barriers& S = *reinterpret_cast<Barriers*>(smem_raw + (size_t)A.stages * A.stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = A.m_tiles * A.n_tiles;
-  const int n_k = A.K / kTileK;                  // also the scale atoms of a 128-row tile
+  const int n_k = A.K / kTileK;                  // also the scale atoms of a 128-row block
+  const uint32_t b_off = PAIR ? kRows128 : (uint32_t)A.a_rows * kTileK;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < A.stages; ++s) {
       mbar_init(&S.full[s], 1);
       mbar_init(&S.empty[s], 1);
     }
     mbar_init(&S.acc_full, 1);
-    mbar_init(&S.acc_empty, kEpiWarps);
+    mbar_init(&S.acc_empty, PAIR ? 2 * kEpiWarps : kEpiWarps);
     mbar_init(&S.mma_done, 1);
     S.failed = 0;
     fence_barrier_init();
   }
   __syncwarp();
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 0) tmem_alloc<PAIR>(&S.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();        // both CTAs' barriers and allocation are in place
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   griddep_wait();
@@ -155,72 +169,97 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- producer
-      uint32_t g = 0;
+      uint32_t s = 0, ph = 1;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      // bytes a CTA brings into a stage
+      const uint32_t bytes = (PAIR ? 2 * kRows128 : b_off + 2 * kRows128) + 3 * kAtom;
+      for (int t = first; t < tiles && ok; t += step) {
         int mt, nt;
         tile_pos(A, t, &mt, &nt);
-        for (int kb = 0; kb < n_k; ++kb, ++g) {
-          const int s = (int)(g % kStages);
-          if (!mbar_wait_bounded(&S.empty[s], ((g / kStages) & 1u) ^ 1u, A.status) || failed_flag(S)) {
+        const int mb = PAIR ? 2 * mt + (int)rank : mt;           // this CTA's 128-row block of A
+        for (int kb = 0; kb < n_k; ++kb) {
+          if (!mbar_wait_bounded(&S.empty[s], ph, A.status) || failed_flag(S)) {
             atomicOr(&S.failed, 1u);
             ok = false;
             break;
           }
-          uint64_t* bar = &S.full[s];
-          mbar_arrive_expect_tx(bar, kStageTx);
-          tma_load_2d(S.a[s], &A.a, kb * kTileK, mt * kTileM, bar);
-          tma_load_2d(S.b[s], &A.g, kb * kTileK, nt * kTileF, bar);
-          tma_load_2d(S.b[s] + kBBytes / 2, &A.u, kb * kTileK, nt * kTileF, bar);
-          bulk_g2s_plain(S.sf[s], A.a_s + ((size_t)mt * n_k + kb) * kAtom, kAtom, bar);
-          bulk_g2s_plain(S.sf[s] + kAtom, A.g_s + ((size_t)nt * n_k + kb) * kAtom, kAtom, bar);
-          bulk_g2s_plain(S.sf[s] + 2 * kAtom, A.u_s + ((size_t)nt * n_k + kb) * kAtom, kAtom, bar);
-          n_issued = g + 1;
+          uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes;
+          uint8_t* sf = sa + A.sf_off;
+          const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * bytes : bytes);
+          tma_load<PAIR>(sa, &A.a, kb * kTileK, mb * 128, bar);
+          if constexpr (PAIR) {
+            tma_load<PAIR>(sa + b_off, &A.w[rank], kb * kTileK, nt * kTileF, bar);
+            // atom (block, kb) is rows 4 * (block * n_k + kb) .. + 3 of the 128-byte-row view; a block of A past the
+            // last has no atom: it repeats the tile's first, for rows that are never stored
+            const int ab = mb * 128 < A.T ? mb : 2 * mt;
+            tma_load<PAIR>(sf, &A.a_sf, 0, 4 * (ab * n_k + kb), bar);
+            tma_load<PAIR>(sf + kAtom, &A.w_sf[0], 0, 4 * (nt * n_k + kb), bar);
+            tma_load<PAIR>(sf + 2 * kAtom, &A.w_sf[1], 0, 4 * (nt * n_k + kb), bar);
+          } else {
+            uint64_t* full = &S.full[s];
+            tma_load<PAIR>(sa + b_off, &A.w[0], kb * kTileK, nt * kTileF, bar);
+            tma_load<PAIR>(sa + b_off + kRows128, &A.w[1], kb * kTileK, nt * kTileF, bar);
+            bulk_g2s_plain(sf, A.a_s + ((size_t)mb * n_k + kb) * kAtom, kAtom, full);
+            bulk_g2s_plain(sf + kAtom, A.w_s[0] + ((size_t)nt * n_k + kb) * kAtom, kAtom, full);
+            bulk_g2s_plain(sf + 2 * kAtom, A.w_s[1] + ((size_t)nt * n_k + kb) * kAtom, kAtom, full);
+          }
+          ++n_issued;
+          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------- MMA
-      uint32_t g = 0, it = 0;
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------ MMA (of a pair: CTA 0)
+      uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
+      auto commit = [&](uint64_t* bar) {         // to both CTAs of a pair
+        if constexpr (PAIR) {
+          tc_commit_pair(smem_u32(bar));
+          tc_commit_pair(cluster_addr(bar, 1));
+        } else {
+          tc_commit(bar);
+        }
+      };
+      for (int t = first; t < tiles && ok; t += step, ++it) {
         if (!mbar_wait_bounded(&S.acc_empty, (it & 1u) ^ 1u, A.status) || failed_flag(S)) {
           atomicOr(&S.failed, 1u);
           ok = false;
           break;
         }
         tc_fence_after();
-        for (int kb = 0; kb < n_k; ++kb, ++g) {
-          const int s = (int)(g % kStages);
-          if (!mbar_wait_bounded(&S.full[s], (g / kStages) & 1u, A.status) || failed_flag(S)) {
+        for (int kb = 0; kb < n_k; ++kb) {
+          if (!mbar_wait_bounded(&S.full[s], ph, A.status) || failed_flag(S)) {
             atomicOr(&S.failed, 1u);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sfa = tmem + kSfCol0 + (uint32_t)s * 12u, sfb = sfa + 4u;
-          for (int j = 0; j < 3; ++j)
-            tmem_cp_sf(sfa + 4u * j, smem_desc(smem_u32(S.sf[s]) + kAtom * j, 0, 128, 0));
-          const uint32_t a0 = smem_u32(S.a[s]), b0 = smem_u32(S.b[s]);
+          const uint32_t a0 = smem_u32(smem_raw) + s * A.stage_bytes, b0 = a0 + b_off, sf = a0 + A.sf_off;
+          const uint32_t sfa = tmem + kSfCol0 + s * 12u, sfb = sfa + 4u;
+#pragma unroll
+          for (int j = 0; j < 3; ++j) tmem_cp_sf<PAIR>(sfa + 4u * j, smem_desc(sf + kAtom * j, 0, 128, 0));
 #pragma unroll
           for (int k = 0; k < kTileK / 32; ++k)
-            mma_mxf8(tmem, smem_desc(a0 + 32u * k, 16, 1024, 2), smem_desc(b0 + 32u * k, 16, 1024, 2),
-                     instr_desc((uint32_t)k), sfa | ((uint32_t)k << 30), sfb | ((uint32_t)k << 30),
-                     (kb > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&S.empty[s]);
+            mma_mxf8<PAIR>(tmem, smem_desc(a0 + 32u * k, 16, 1024, 2), smem_desc(b0 + 32u * k, 16, 1024, 2),
+                           instr_desc(PAIR ? 256 : 128, (uint32_t)k), sfa | ((uint32_t)k << 30), sfb | ((uint32_t)k << 30),
+                           (kb > 0 || k > 0) ? 1u : 0u);
+          commit(&S.empty[s]);
+          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
         }
-        if (ok) tc_commit(&S.acc_full);
+        if (ok) commit(&S.acc_full);
       }
-      tc_commit(&S.mma_done);
-      if (!ok) tc_commit(&S.acc_full);           // wake the epilogue; it sees the failure
+      if constexpr (PAIR) tc_commit_pair(smem_u32(&S.mma_done));
+      else tc_commit(&S.mma_done);
+      if (!ok) commit(&S.acc_full);              // wake the epilogues; they see the failure or time out
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;            // features 64 * half .. of the tile
     uint32_t it = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+    for (int t = first; t < tiles; t += step, ++it) {
       int mt, nt;
       tile_pos(A, t, &mt, &nt);
       const bool got = mbar_wait_bounded(&S.acc_full, it & 1u, A.status);
@@ -242,8 +281,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
       tmem_ld_fence(u[1], false);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.acc_empty);  // the MMA thread may overwrite the accumulator
-      const int row = mt * kTileM + quarter * 32 + lane;
+      if (lane == 0) {                           // the MMA thread may overwrite the accumulator
+        if (rank == 0) mbar_arrive(&S.acc_empty);
+        else mbar_arrive_remote(cluster_addr(&S.acc_empty, 0));
+      }
+      const int row = (PAIR ? 2 * mt + (int)rank : mt) * 128 + quarter * 32 + lane;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int col = nt * kTileF + half * 64 + 32 * j;
@@ -262,28 +304,33 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 1 && lane == 0) mbar_wait_bounded(&S.mma_done, 0, A.status);
-  if (warp == 0 && lane == 0 && failed_flag(S))  // leave no copy in flight
-    for (uint32_t j = (n_issued > (uint32_t)kStages ? n_issued - kStages : 0); j < n_issued; ++j)
-      mbar_wait_bounded(&S.full[j % kStages], (j / kStages) & 1u, A.status);
+  if (warp == 1 && lane == 0 && rank == 0) mbar_wait_bounded(&S.mma_done, 0, A.status);
+  if (warp == 0 && lane == 0 && rank == 0 && failed_flag(S))   // leave no copy in flight
+    for (uint32_t j = (n_issued > (uint32_t)A.stages ? n_issued - A.stages : 0); j < n_issued; ++j)
+      mbar_wait_bounded(&S.full[j % A.stages], (j / A.stages) & 1u, A.status);
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();        // no MMA, copy or remote arrive into either CTA remains
   tc_fence_after();
-  if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  if (warp == 0) tmem_free<PAIR>(tmem, kTmemCols);
 }
 
-// 2-D map over a row-major uint8 [rows, cols] matrix, boxes of 128 rows x 128 bytes, 128-byte swizzle.
-bool make_map(CUtensorMap* map, const void* base, int rows, int cols) {
+// 2-D map over a row-major uint8 [rows, cols] matrix, boxes of box_rows x 128 bytes, 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows, bool swizzle = true) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)cols};
-  const cuuint32_t box[2] = {(cuuint32_t)kTileK, 128};
+  const cuuint32_t box[2] = {(cuuint32_t)kTileK, (cuuint32_t)box_rows};
   const cuuint32_t elem[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A scale array of a [rows, K] operand as rows of 128 bytes: an atom is a box of 4.
+bool make_sf_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K) {
+  return make_map(map, base, (rows + 127) / 128 * (K / kTileK) * 4, 128, 4, false);
 }
 
 }  // namespace
@@ -292,43 +339,79 @@ int gated_mxfp8_launch(const void* a_q, const void* a_s, const void* g_q, const 
                        const void* u_s, void* h, void* h_s, int T, int F, int K, int act, bool scale_mma, int sms,
                        unsigned* status, cudaStream_t stream, const char** why) {
   Args A{};
-  if (!make_map(&A.a, a_q, T, K) || !make_map(&A.g, g_q, F, K) || !make_map(&A.u, u_q, F, K)) {
-    *why = "cuTensorMapEncodeTiled failed";
-    return -1;
-  }
   A.a_s = static_cast<const uint8_t*>(a_s);
-  A.g_s = static_cast<const uint8_t*>(g_s);
-  A.u_s = static_cast<const uint8_t*>(u_s);
+  A.w_s[0] = static_cast<const uint8_t*>(g_s);
+  A.w_s[1] = static_cast<const uint8_t*>(u_s);
   A.h = static_cast<uint8_t*>(h);
   A.h_s = static_cast<uint8_t*>(h_s);
   A.status = status;
   A.T = T;
   A.F = F;
   A.K = K;
-  A.m_tiles = (T + kTileM - 1) / kTileM;
-  A.n_tiles = (F + kTileF - 1) / kTileF;
   A.act = act;
   A.out = !h_s ? 0 : (scale_mma ? 2 : 1);
-  const int64_t tiles = (int64_t)A.m_tiles * A.n_tiles;
+  A.n_tiles = (F + kTileF - 1) / kTileF;
+  constexpr size_t kCap = 227 * 1024 - 512;
+  static_assert(sizeof(Barriers) <= 512, "barrier block");
+
+  // Pairs where their 256-row tiles take fewer rounds of tile time (twice the
+  // work of a 128-row tile on two SMs).
+  const void* kernel = (const void*)gated_mxfp8_kernel<true>;
+  constexpr uint32_t kPairStage = 2 * kRows128 + 2048;             // 1024-aligned
+  constexpr int kPairStages = (int)(kCap / kPairStage) < kMaxStages ? (int)(kCap / kPairStage) : kMaxStages;
+  constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + sizeof(Barriers);
+  int pairs = 0;
+  if (T > 128) {
+    pairs = cta_pair_capacity(kernel, kThreads, kPairSmem, 3);
+    if (pairs > sms / 2) pairs = sms / 2;
+  }
+  const int64_t t1 = (int64_t)((T + 127) / 128) * A.n_tiles, t2 = (int64_t)((T + 255) / 256) * A.n_tiles;
+  const bool pair = pairs > 0 && (t2 + pairs - 1) / pairs <= (t1 + sms - 1) / sms;
+  const int64_t tiles = pair ? t2 : t1;
   if (tiles > 0x7FFFFFFF - sms) {
     *why = "too many tiles";
     return -1;
   }
-  const size_t smem = sizeof(Smem);
-  cudaError_t e = cudaFuncSetAttribute(gated_mxfp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  A.m_tiles = pair ? (T + 255) / 256 : (T + 127) / 128;
+  A.a_rows = pair || T >= 128 ? 128 : (T + 7) / 8 * 8;
+  size_t smem;
+  if (pair) {
+    A.sf_off = 2 * kRows128;
+    A.stage_bytes = kPairStage;
+    A.stages = kPairStages;
+    smem = kPairSmem;
+  } else {
+    kernel = (const void*)gated_mxfp8_kernel<false>;
+    A.sf_off = (uint32_t)A.a_rows * kTileK + 2 * kRows128;
+    A.stage_bytes = A.sf_off + 2048;
+    A.stages = (int)(kCap / A.stage_bytes);
+    if (A.stages > kMaxStages) A.stages = kMaxStages;
+    smem = (size_t)A.stages * A.stage_bytes + sizeof(Barriers);    // B's 32 KiB cover the last stage's A window
+  }
+  if (!make_map(&A.a, a_q, T, K, A.a_rows) || !make_map(&A.w[0], g_q, F, K, 128) || !make_map(&A.w[1], u_q, F, K, 128) ||
+      (pair && (!make_sf_map(&A.a_sf, a_s, T, K) || !make_sf_map(&A.w_sf[0], g_s, F, K) || !make_sf_map(&A.w_sf[1], u_s, F, K)))) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return -1;
+  }
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) { *why = cudaGetErrorString(e); return (int)e; }
   void* argv[] = {&A};
+  const int units = pair ? pairs : sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles < sms ? (int)tiles : sms);
+  cfg.gridDim = dim3((unsigned)((tiles < units ? (int)tiles : units) * (pair ? 2 : 1)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelExC(&cfg, (const void*)gated_mxfp8_kernel, argv);
+  cfg.numAttrs = pair ? 2 : 1;
+  e = cudaLaunchKernelExC(&cfg, kernel, argv);
   if (e != cudaSuccess) { *why = cudaGetErrorString(e); return (int)e; }
   return 0;
 }
