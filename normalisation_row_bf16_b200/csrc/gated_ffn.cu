@@ -332,12 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
       bool ok = true;
       const uint32_t idesc = instr_desc(PAIR ? 256 : 128, A.acc_n, kAmn, kBmn);
       auto commit = [&](uint64_t* bar) {         // to both CTAs of a pair
-        if constexpr (PAIR) {
-          tc_commit_pair(smem_u32(bar));
-          tc_commit_pair(cluster_addr(bar, 1));
-        } else {
-          tc_commit(bar);
-        }
+        if constexpr (PAIR) tc_commit_both(smem_u32(bar));
+        else tc_commit(bar);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok && (!mbar_wait_bounded(bar, parity, A.status) || failed_flag(S))) {

@@ -215,13 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
       uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
       auto commit = [&](uint64_t* bar) {         // to both CTAs of a pair
-        if constexpr (PAIR) {
-          tc_commit_pair(smem_u32(bar));
-          tc_commit_pair(cluster_addr(bar, 1));
-        } else {
-          tc_commit(bar);
-        }
+        if constexpr (PAIR) tc_commit_both(smem_u32(bar));
+        else tc_commit(bar);
       };
+      const uint32_t base = smem_u32(smem_raw);
+      const uint64_t a_desc = smem_desc(base, 16, 1024, 2), b_desc = smem_desc(base + b_off, 16, 1024, 2),
+                     sf_desc = smem_desc(base + A.sf_off, 0, 128, 0);
       for (int t = first; t < tiles && ok; t += step, ++it) {
         if (!mbar_wait_bounded(&S.acc_empty, (it & 1u) ^ 1u, A.status) || failed_flag(S)) {
           atomicOr(&S.failed, 1u);
@@ -230,21 +229,21 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
         }
         tc_fence_after();
         for (int kb = 0; kb < n_k; ++kb) {
-          if (!mbar_wait_bounded(&S.full[s], ph, A.status) || failed_flag(S)) {
+          if (!mbar_wait_bounded(&S.full[s], ph, A.status)) {
             atomicOr(&S.failed, 1u);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem_raw) + s * A.stage_bytes, b0 = a0 + b_off, sf = a0 + A.sf_off;
+          // descriptors: the start address (>> 4) is the low field
+          const uint64_t at = (uint64_t)(s * (A.stage_bytes >> 4));
           const uint32_t sfa = tmem + kSfCol0 + s * 12u, sfb = sfa + 4u;
 #pragma unroll
-          for (int j = 0; j < 3; ++j) tmem_cp_sf<PAIR>(sfa + 4u * j, smem_desc(sf + kAtom * j, 0, 128, 0));
+          for (int j = 0; j < 3; ++j) tmem_cp_sf<PAIR>(sfa + 4u * j, sf_desc + at + j * (kAtom >> 4));
 #pragma unroll
           for (int k = 0; k < kTileK / 32; ++k)
-            mma_mxf8<PAIR>(tmem, smem_desc(a0 + 32u * k, 16, 1024, 2), smem_desc(b0 + 32u * k, 16, 1024, 2),
-                           instr_desc(PAIR ? 256 : 128, (uint32_t)k), sfa | ((uint32_t)k << 30), sfb | ((uint32_t)k << 30),
-                           (kb > 0 || k > 0) ? 1u : 0u);
+            mma_mxf8<PAIR>(tmem, a_desc + at + 2 * k, b_desc + at + 2 * k, instr_desc(PAIR ? 256 : 128, (uint32_t)k),
+                           sfa | ((uint32_t)k << 30), sfb | ((uint32_t)k << 30), (kb > 0 || k > 0) ? 1u : 0u);
           commit(&S.empty[s]);
           if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
         }
