@@ -353,16 +353,18 @@ int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, 
  * dh, gate, up bf16 [T, F] dense; x, w_gate, w_up, D, F, ld as in gated_ffn_fwd.
  * dx      bf16 [T, D] (written) or NULL
  * dw_gate, dw_up  bf16 [F, D] (written), or both NULL.  T = 0 writes zeros.
- * Sums are fp32 in tensor memory, in a fixed order: no atomics.
- * workspace  device scratch of at least gated_ffn_bwd_workspace_size(T, F)
+ * Sums are fp32, in a fixed order: no atomics.
+ * workspace  device scratch of at least gated_ffn_bwd_workspace_size(T, D, F)
  *         bytes, 16-byte aligned.  Contents on entry are ignored.
  */
 int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
                   const void* up, void* dx, void* dw_gate, void* dw_up, int64_t T, int64_t D, int64_t F, int64_t ld_x,
                   int64_t ld_w, int act, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Scratch bytes gated_ffn_bwd needs: dg and du (0 if the arguments are invalid). */
-size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t F);
+/* Scratch bytes gated_ffn_bwd needs on the current device: dg and du, and
+   partial sums of dx where few rows leave SMs idle (0 if the arguments are
+   invalid). */
+size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t D, int64_t F);
 
 /* Output of mxfp8_gated_ffn. */
 enum mxn_ffn_out {

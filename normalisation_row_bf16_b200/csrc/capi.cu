@@ -888,9 +888,11 @@ int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, 
   return MXN_OK;
 }
 
-size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t F) {
-  if (T <= 0 || F <= 0 || F % 8 || T > kFfnMax || F > kFfnMax) return 0;
-  return (size_t)2 * sizeof(uint16_t) * (size_t)T * (size_t)F;
+size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t D, int64_t F) {
+  if (T <= 0 || check_ffn(T, D, F, D, D, MXN_ACT_SILU)) return 0;
+  DeviceInfo dev;
+  if (device_info(&dev)) return 0;
+  return gated_ffn_bwd_workspace((int)T, (int)D, (int)F, dev.sms);
 }
 
 int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
@@ -917,16 +919,18 @@ int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void*
     return MXN_OK;
   }
   if (!dx && !dw_gate) return MXN_OK;
-  const size_t need = gated_ffn_bwd_workspace_size(T, F);
   if (!workspace || !aligned16(workspace)) return fail(MXN_ERR_ARG, "workspace is NULL or not 16-byte aligned");
-  if (workspace_bytes < need)
-    return fail(MXN_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t least = (size_t)2 * sizeof(uint16_t) * (size_t)T * (size_t)F;      // known without a device
+  if (workspace_bytes < least)
+    return fail(MXN_ERR_ARG, "workspace of %zu bytes, at least %zu needed", workspace_bytes, least);
   DeviceInfo dev;
   if ((rc = device_info(&dev))) return rc;
-  uint16_t* dg = static_cast<uint16_t*>(workspace);
+  const size_t need = gated_ffn_bwd_workspace((int)T, (int)D, (int)F, dev.sms);
+  if (workspace_bytes < need)
+    return fail(MXN_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   const char* why = "";
-  const int e = gated_ffn_bwd_launch(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, dg, dg + T * F, (int)T,
-                                     (int)D, (int)F, ld_x, ld_w, act, dev.sms, dev.status, s, &why);
+  const int e = gated_ffn_bwd_launch(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace, (int)T, (int)D,
+                                     (int)F, ld_x, ld_w, act, dev.sms, dev.status, s, &why);
   if (e) return fail(MXN_ERR_CUDA, "gated_ffn_bwd: %s", why);
   return MXN_OK;
 }

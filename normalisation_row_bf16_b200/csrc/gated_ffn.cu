@@ -41,6 +41,7 @@ constexpr int kGroupM = 8;                       // tiles go m-first inside grou
 struct Args {
   CUtensorMap a[2], b[2], c[3];                  // c: outputs, of pairs
   uint16_t* out[3];      // kGate: h, gate, up (the last two may be null); kDx: dx; kDw: dWg, dWu
+  float* partial;        // kDx with more than one problem: fp32 [problems, M, N] in place of dx
   unsigned* status;
   int64_t ld_out;
   int problems;
@@ -131,12 +132,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Work unit t of the launch: problem, first output row, tile column, and for
-// pairs the 256-row halves it covers.
 // Pairs: units of the last 256-row half when there is an odd number of them.
 __host__ __device__ __forceinline__ int odd_halves(const Args& A) {
   return A.m_halves & 1 ? A.problems * A.n_tiles : 0;
 }
+// Work unit t of the launch: problem, first output row, tile column, and for
+// pairs the 256-row halves it covers.
 struct TilePos {
   int p, m0, nt, halves;
 };
@@ -173,6 +174,25 @@ __device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
   }
   q.halves = 1;
   return q;
+}
+
+// K stages [k_lo, k_hi) of problem p.  kDx deals its contraction to `problems`
+// partial products of the same output.
+template <int MODE>
+__device__ __forceinline__ int k_lo(const Args& A, int p) {
+  return MODE == kDx ? (int)((int64_t)p * A.n_k / A.problems) : 0;
+}
+template <int MODE>
+__device__ __forceinline__ int k_hi(const Args& A, int p) {
+  return MODE == kDx ? (int)((int64_t)(p + 1) * A.n_k / A.problems) : A.n_k;
+}
+
+// 16 fp32 columns of one row of a partial product, those below n (a multiple of 8).
+__device__ __forceinline__ void store_cols16_f32(float* row, int col, int n, const uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + 4 * i < n)
+      *reinterpret_cast<uint4*>(row + col + 4 * i) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
 }
 
 // 16 output columns of one row, from col on, those below n (a multiple of 8).
@@ -286,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
         const TilePos q = tile_pos<PAIR>(A, t);
         // bytes of a stage: tiles of one half leave A's second block out
         const uint32_t bytes = PAIR && q.halves == 1 ? A.stage_bytes - kABytes : A.stage_bytes;
-        for (int kb = 0; kb < A.n_k; ++kb) {
+        const int k_end = k_hi<MODE>(A, q.p);
+        for (int kb = k_lo<MODE>(A, q.p); kb < k_end; ++kb) {
           if (!mbar_wait_bounded(&S.empty[s], ph, A.status) || failed_flag(S)) {
             atomicOr(&S.failed, 1u);
             ok = false;
@@ -351,10 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           mma_bf16<PAIR>(tmem + acc * 256u, op_desc(a0, k, kAmn), op_desc(b0, k, kBmn), idesc, (!first_k || k > 0) ? 1u : 0u);
       };
       for (int t = first; t < A.tiles && ok; t += step, ++it) {
+        const TilePos q = tile_pos<PAIR>(A, t);
+        const int n_k = k_hi<MODE>(A, q.p) - k_lo<MODE>(A, q.p);
         if constexpr (!PAIR) {
           const uint32_t acc = it & 1u;
           wait(&S.acc_empty[acc], (uses[acc]++ & 1u) ^ 1u);
-          for (int kb = 0; kb < A.n_k && ok; ++kb) {
+          for (int kb = 0; kb < n_k && ok; ++kb) {
             wait(&S.full[s], ph);
             if (!ok) break;
             mma_stage(s, 0, acc, kb == 0);
@@ -363,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           }
           if (ok) commit(&S.acc_full[acc]);
         } else {
-          const int halves = tile_pos<PAIR>(A, t).halves;
-          const int lead = halves == 2 ? min(A.n_k, A.stages) : 0;   // stages that go to the first accumulator alone
+          const int halves = q.halves;
+          const int lead = halves == 2 ? min(n_k, A.stages) : 0;   // stages that go to the first accumulator alone
           wait(&S.acc_empty[0], (uses[0]++ & 1u) ^ 1u);
           uint32_t s1 = s;
           for (int kb = 0; kb < lead && ok; ++kb) {
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
               if (++s1 == (uint32_t)A.stages) s1 = 0;
             }
           }
-          for (int kb = lead; kb < A.n_k && ok; ++kb) {
+          for (int kb = lead; kb < n_k && ok; ++kb) {
             wait(&S.full[s], ph);
             if (!ok) break;
             mma_stage(s, 0, 0, kb == 0);
@@ -460,6 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
               }
             } else {
               tmem_ld16_fence(r, true);
+              if (MODE == kDx && A.partial) {
+                if (live) store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row) * A.N, col, end, r);
+                __syncwarp();
+                continue;
+              }
               pack16(r, o);
               if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, end, o);
             }
@@ -509,6 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             tmem_ld16_fence(r[0], true);
 #pragma unroll
             for (int c = 1; c < 4; ++c) tmem_ld16_fence(r[c], false);
+            if (MODE == kDx && A.partial) {
+              if (row0 + lane < A.M) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row0 + lane) * A.N, col0 + 16 * c, A.N, r[c]);
+              }
+              __syncwarp();
+              continue;
+            }
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
 #pragma unroll
@@ -573,6 +610,23 @@ __global__ void __launch_bounds__(256) gated_act_bwd_kernel(const uint16_t* dh, 
   }
 }
 
+// dx = bf16 of the sum of the partial products [parts, n] in order: 8 elements a thread.
+__global__ void __launch_bounds__(256) gated_sum_kernel(const float* partial, int parts, int64_t n, uint16_t* dx) {
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int64_t i = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x); i < n; i += 8 * (int64_t)gridDim.x * blockDim.x) {
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float4 x = *reinterpret_cast<const float4*>(partial + p * n + i);
+      const float4 y = *reinterpret_cast<const float4*>(partial + p * n + i + 4);
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    }
+    *reinterpret_cast<uint4*>(dx + i) = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+  }
+}
+
 // ------------------------------------------------------------------- launches
 
 // 2-D map over a row-major bf16 [rows, cols] matrix of row stride ld, boxes of
@@ -631,48 +685,73 @@ const void* kernel_of(int mode, bool pair) {
   return mode == kGate ? kernel_of<kGate>(pair) : mode == kDx ? kernel_of<kDx>(pair) : kernel_of<kDw>(pair);
 }
 
-// Fills the tile and ring geometry of a launch.  Returns false when the tiles
-// outnumber an int.
+// Fills the tile and ring geometry of a launch from A's M, N and n_k.  Returns
+// false when the tiles outnumber an int.
+//
+// The shape with the least estimated time, from figures measured on B200: a
+// single CTA's K stage takes as long as its bytes at 90 GB/s an SM, and a
+// twelfth of the 2.5 us a ring takes around at least; a pair's 0.46 us for a
+// 256-row half and 0.77 for a whole tile; a tile 2.5 to 3 us more; and all
+// operands come from HBM once.  kDx may deal the contraction to up to 8 partial
+// products, which another kernel adds up (3 us and their bytes at 6 TB/s):
+// without it 333 x 1032 x 2744 took 25 us on 51 of 148 SMs.
 bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
-  const int unit = mode == kGate ? 8 : 64, widest = mode == kGate ? 128 : 256;
-  A.problems = problems;
-  // Single CTAs: the tile width that divides the columns over the SMs in the
-  // fewest rounds of equal cost; a tile costs its columns, and its rows of A
-  // half as much (they come from L2).
-  A.a_rows = mode == kDw || A.M >= 128 ? 128 : (A.M + 7) / 8 * 8;
-  int64_t best = 0;
-  for (int w = widest; w >= unit; w -= unit) {
-    const int64_t tiles = (int64_t)cdiv(A.M, 128) * cdiv(A.N, w) * problems;
-    const int64_t cost = ((tiles + sms - 1) / sms) * ((mode == kGate ? 2 * w : w) + A.a_rows / 2);
-    if (best == 0 || cost < best) {
-      best = cost;
-      A.tile_n = w;
-    }
-  }
-  L->pair = false;
-  // Pairs.
   constexpr uint32_t kPairStage = 3 * kABytes;
   constexpr int kPairStages = (int)((kSmemCap - kEpiWarps * kBoxBytes) / kPairStage);
   constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + kEpiWarps * kBoxBytes + sizeof(Barriers);
+  const int unit = mode == kGate ? 8 : 64, widest = mode == kGate ? 128 : 256;
+  A.a_rows = mode == kDw || A.M >= 128 ? 128 : (A.M + 7) / 8 * 8;
   int pairs = 0;
   if (A.M > 128) {
     pairs = cta_pair_capacity(kernel_of(mode, true), kThreads, kPairSmem, mode);
     if (pairs > sms / 2) pairs = sms / 2;
-    const int64_t tiles = (int64_t)cdiv(A.M, 256) * cdiv(A.N, widest) * problems;
-    const int64_t cost = pairs ? ((tiles + pairs - 1) / pairs) * 256 : best;
-    if (cost < best) {
-      L->pair = true;
-      A.tile_n = widest;
+  }
+  const double hbm = 128.0 * A.n_k * (A.M + (double)A.N * (mode == kGate ? 2 : 1)) * (mode == kDw ? 2 : 1) / 6.5e6;
+  double best = 0;
+  auto better = [&](double us) {
+    if (best != 0 && us > best) return false;      // equal: the narrower tile, on more SMs
+    best = us;
+    return true;
+  };
+  for (int split = 1; split <= (mode == kDx ? 8 : 1) && (split == 1 || A.n_k / split >= 4); ++split) {
+    const int probs = problems * split;
+    const double nk = (double)A.n_k / split;
+    const double sum = split > 1 ? 3.0 + 8.0 * split * A.M * A.N / 6e6 : 0.0;
+    for (int w = widest; w >= unit; w -= unit) {
+      const int64_t tiles = (int64_t)cdiv(A.M, 128) * cdiv(A.N, w) * probs, rounds = (tiles + sms - 1) / sms;
+      // the second operand streams from HBM where only one row of tiles reads it
+      const bool cold = A.M <= 128;
+      double kb = (A.a_rows / 90e3 + (mode == kGate ? 2 * w : w) / (cold ? 60e3 : 90e3)) * 128;
+      if (kb < 2.5 / kMaxStages) kb = 2.5 / kMaxStages;
+      const double stream = rounds * nk * kb;
+      if (better((stream > hbm ? stream : hbm) + rounds * 2.5 + sum)) {
+        L->pair = false;
+        A.tile_n = w;
+        A.problems = probs;
+      }
+    }
+    if (pairs > 0) {
+      const int64_t n_tiles = (int64_t)cdiv(A.N, widest) * probs, halves = cdiv(A.M, 256);
+      const int64_t whole = halves / 2 * n_tiles, odd = (halves & 1) * n_tiles, rest = whole % pairs;
+      const double t1 = nk * 0.46 + 3.0, t2 = nk * 0.77 + 3.0;
+      const double us = 2 * rest + odd <= pairs
+                            ? (double)(whole / pairs) * t2 + (rest || odd ? t1 : 0.0)
+                            : (double)((whole + pairs - 1) / pairs) * t2 + (double)((odd + pairs - 1) / pairs) * t1;
+      if (better((us > hbm ? us : hbm) + sum)) {
+        L->pair = true;
+        A.tile_n = widest;
+        A.problems = probs;
+      }
     }
   }
   A.n_tiles = cdiv(A.N, A.tile_n);
   A.m_tiles = cdiv(A.M, L->pair ? 256 : 128);
-  int64_t tiles = (int64_t)A.m_tiles * A.n_tiles * problems;
+  int64_t tiles = (int64_t)A.m_tiles * A.n_tiles * A.problems;
   if (tiles > 0x7FFFFFFF - sms) return false;
   if (L->pair) {
     A.m_halves = A.m_tiles;
     A.m_tiles = A.m_halves / 2;
-    const int64_t whole = (int64_t)A.m_tiles * A.n_tiles * problems, odd = odd_halves(A);
+    const int64_t whole = (int64_t)A.m_tiles * A.n_tiles * A.problems, odd = odd_halves(A);
     const int64_t rest = whole % pairs;          // past the last full round
     A.whole = (int)(2 * rest + odd <= pairs ? whole - rest : whole);
     tiles = A.whole + 2 * (whole - A.whole) + odd;
@@ -696,6 +775,18 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   L->kernel = kernel_of(mode, L->pair);
   return true;
 }
+
+// The plan of dx [T, D] = [dg du] [Wg; Wu].
+bool plan_dx(Args& A, int T, int D, int F, int sms, Launch* L) {
+  A.M = T;
+  A.N = D;
+  A.n_k0 = cdiv(F, kTileK);
+  A.n_k = 2 * A.n_k0;
+  return plan_tiles(A, kDx, 1, sms, L);
+}
+
+// Bytes of dg and du, rounded up so that what follows stays aligned.
+size_t grads_bytes(int T, int F) { return ((size_t)4 * T * F + 255) / 256 * 256; }
 
 int launch_gemm(const Launch& L, Args& A, cudaStream_t stream, const char* what, const char** why) {
   void* argv[] = {&A};
@@ -761,15 +852,23 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
   return launch_gemm(L, A, stream, "gated_ffn_fwd launch", why);
 }
 
+size_t gated_ffn_bwd_workspace(int T, int D, int F, int sms) {
+  Args A{};
+  Launch L;
+  if (!plan_dx(A, T, D, F, sms, &L)) return 0;
+  return grads_bytes(T, F) + (A.problems > 1 ? (size_t)A.problems * T * D * sizeof(float) : 0);
+}
+
 int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
-                         const void* up, void* dx, void* dw_gate, void* dw_up, void* dg, void* du, int T, int D,
-                         int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
+                         const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace, int T, int D, int F,
+                         int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
                          const char** why) {
+  uint16_t* dg = static_cast<uint16_t*>(workspace);
+  uint16_t* du = dg + (int64_t)T * F;
   const uint16_t *dhp = static_cast<const uint16_t*>(dh), *gp = static_cast<const uint16_t*>(gate),
                  *upp = static_cast<const uint16_t*>(up);
-  uint16_t *dgp = static_cast<uint16_t*>(dg), *dup = static_cast<uint16_t*>(du);
   int64_t n8 = (int64_t)T * F / 8;
-  void* argv[] = {&dhp, &gp, &upp, &dgp, &dup, &n8};
+  void* argv[] = {&dhp, &gp, &upp, &dg, &du, &n8};
   const int64_t blocks = (n8 + 255) / 256, most = (int64_t)sms * 8;
   const void* k = act == kActSilu ? (const void*)gated_act_bwd_kernel<kActSilu>
                                   : (act == kActGelu ? (const void*)gated_act_bwd_kernel<kActGelu>
@@ -778,15 +877,12 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
   if (e) return e;
   if (dx) {
     Args A{};
+    Launch L;
     A.out[0] = static_cast<uint16_t*>(dx);
     A.status = status;
     A.ld_out = D;
-    A.M = T;
-    A.N = D;
-    A.n_k0 = cdiv(F, kTileK);
-    A.n_k = 2 * A.n_k0;
-    Launch L;
-    if (!plan_tiles(A, kDx, 1, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (!plan_dx(A, T, D, F, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (A.problems > 1) A.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grads_bytes(T, F));
     if (!make_map(&A.a[0], dg, T, F, F, A.a_rows) || !make_map(&A.a[1], du, T, F, F, A.a_rows) ||
         !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK) ||
         (L.pair && !make_out_maps(A))) {
@@ -795,6 +891,16 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     }
     e = launch_gemm(L, A, stream, "gated_ffn_bwd dx launch", why);
     if (e) return e;
+    if (A.partial) {
+      const float* partial = A.partial;
+      int64_t n = (int64_t)T * D;
+      uint16_t* out = A.out[0];
+      void* args[] = {&partial, &A.problems, &n, &out};
+      const int64_t need = (n / 8 + 255) / 256, cap = (int64_t)sms * 8;
+      e = launch_pdl((const void*)gated_sum_kernel, (int)(need < cap ? need : cap), 256, 0, args, stream,
+                     "gated_ffn_bwd sum launch", why);
+      if (e) return e;
+    }
   }
   if (dw_gate) {
     Args A{};

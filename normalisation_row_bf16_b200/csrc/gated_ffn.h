@@ -15,10 +15,14 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
                          int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
                          cudaStream_t stream, const char** why);
 
-// dg, du: bf16 [T, F] scratch.  dx, and the pair dw_gate, dw_up, may be null.
+// Scratch of the backward: dg and du, and dx's partial products where it splits
+// the contraction.
+size_t gated_ffn_bwd_workspace(int T, int D, int F, int sms);
+
+// dx, and the pair dw_gate, dw_up, may be null.
 int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
-                         const void* up, void* dx, void* dw_gate, void* dw_up, void* dg, void* du, int T, int D,
-                         int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
+                         const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace, int T, int D, int F,
+                         int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
                          const char** why);
 
 }  // namespace mxn

@@ -48,7 +48,7 @@ SIGNATURES = {
     "layernorm_bwd_workspace_size": (_SZ, [_I64, _I64, _I32]),
     "gated_ffn_fwd": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P]),
     "gated_ffn_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P, _SZ, _P]),
-    "gated_ffn_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "gated_ffn_bwd_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "mxfp8_gated_ffn": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P]),
     "mxnorm_last_error": (ctypes.c_char_p, []),
     "mxnorm_device_status": (_I32, [_P]),
@@ -483,8 +483,8 @@ def _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, stream):
     return h, gate, up
 
 
-def gated_ffn_bwd_workspace_bytes(T: int, F: int) -> int:
-    return int(lib().gated_ffn_bwd_workspace_size(T, F))
+def gated_ffn_bwd_workspace_bytes(T: int, D: int, F: int) -> int:
+    return int(lib().gated_ffn_bwd_workspace_size(T, D, F))
 
 
 def gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None, dw_gate=None, dw_up=None,
@@ -510,7 +510,7 @@ def _gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, works
     if want_dw or dw_gate is not None or dw_up is not None:
         dw_gate = _output(dw_gate, "dw_gate", (F, D), torch.bfloat16, x)
         dw_up = _output(dw_up, "dw_up", (F, D), torch.bfloat16, x)
-    workspace = _workspace(workspace, gated_ffn_bwd_workspace_bytes(T, F), x)
+    workspace = _workspace(workspace, gated_ffn_bwd_workspace_bytes(T, D, F), x)
     _check(lib().gated_ffn_bwd(ph, *ptrs, pg, pu, _addr(dx), _addr(dw_gate), _addr(dw_up), *dims, ACT[act],
                                workspace.data_ptr(), workspace.nbytes, stream))
     return dx, dw_gate, dw_up

@@ -89,8 +89,8 @@ def test_host_fault_injection(L):
 
 
 def test_workspace_sizes(L):
-    assert L.gated_ffn_bwd_workspace_size(100, 64) == 4 * 100 * 64
-    assert L.gated_ffn_bwd_workspace_size(0, 64) == 0 and L.gated_ffn_bwd_workspace_size(4, 60) == 0
+    assert L.gated_ffn_bwd_workspace_size(0, 64, 64) == 0 and L.gated_ffn_bwd_workspace_size(4, 64, 60) == 0
+    assert L.gated_ffn_bwd_workspace_size(4, 60, 64) == 0
     assert L.layernorm_bwd_workspace_size(4, 16385, 0) == 0 and L.layernorm_bwd_workspace_size(4, 64, 3) == 0
     assert L.layernorm_bwd_workspace_size(0, 64, 0) == 0
 
