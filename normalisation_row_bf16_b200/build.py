@@ -1,4 +1,5 @@
-"""Builds libmxnorm_b200.so in-tree with nvcc for sm_100a (no JIT cache).
+"""Builds libmxnorm_b200.so in-tree with nvcc for sm_100a (no JIT cache), and the
+Python module that marshals torch tensors for it (_binding.so, host code only).
 
     python -m normalisation_row_bf16_b200.build
 """
@@ -14,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxnorm_b200.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xptxas", "-warn-spills"]
 
@@ -23,11 +26,19 @@ def sources():
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def is_stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(target: str, srcs) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(s) > t for s in srcs)
+
+
+def is_stale() -> bool:
+    return _older(LIB, sources())
+
+
+def binding_is_stale() -> bool:
+    return _older(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def nvcc() -> str:
@@ -37,8 +48,39 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def _start_binding(verbose: bool):
+    """Starts the compiler on the binding module: (process, temporary output)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = BINDING + f".tmp{os.getpid()}"
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    inc += cpp_extension.include_paths()
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-I" + i for i in inc], "-o", tmp, BINDING_SRC,
+           "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    return subprocess.Popen(cmd), tmp
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every translation unit in csrc/ (in parallel) and link the library."""
+    """Compile every translation unit in csrc/ (in parallel) and link the
+    library, and the binding module beside it."""
+    binding = _start_binding(verbose) if force or binding_is_stale() else None
+    try:
+        return _build_library(force, verbose)
+    finally:
+        if binding:
+            if binding[0].wait() != 0:
+                raise RuntimeError("the binding module did not compile")
+            os.replace(binding[1], BINDING)
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and not is_stale():
         return LIB
     tus = sorted(glob.glob(os.path.join(CSRC, "*.cu")))

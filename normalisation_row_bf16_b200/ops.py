@@ -7,8 +7,8 @@ tensors, raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -305,73 +305,47 @@ def mxfp8_gemm(a_q, a_s, b_q, b_s, M: int, N: int, K: int, c=None, stream=None):
     return c
 
 
-# The host's share of a small call counts as much as the kernel's: checks below
-# read each property once, and the default stream is asked for as a raw handle.
+# The operators below marshal their arguments in compiled code (csrc/binding.cpp):
+# the host's share of a small call counts as much as its kernel's.
 
-def _input(t, name, shape, dtype, dev, dense: bool = True):
-    """Checks an input tensor: shape, type, CUDA device index; rows (the last
-    dimension) contiguous, with `dense` the whole tensor.  Its data pointer."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_contiguous():
-        if dense:
-            raise ValueError(f"{name} must be contiguous")
-        if t.stride(-1) != 1 and shape[-1] != 1:
-            raise ValueError(f"rows of {name} must be contiguous")
-    return t.data_ptr()
+_binding_module = None
 
 
-def _ld(t):
-    """Row stride of a 2-D tensor (its width where it has at most one row)."""
-    rows, cols = t.shape
-    return t.stride(0) if rows > 1 else cols
+def _binding():
+    """The binding module, holding the loaded library's entry points; raises if
+    either has not been built."""
+    global _binding_module
+    if _binding_module is None:
+        L = lib()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"{_build.BINDING} is missing: run `python -m normalisation_row_bf16_b200.build` "
+                               "(there is no CPU fallback)")
+        spec = importlib.util.spec_from_file_location("normalisation_row_bf16_b200._binding", _build.BINDING)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        names = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_size", "gated_ffn_fwd", "gated_ffn_bwd",
+                 "gated_ffn_bwd_workspace_size", "mxfp8_gated_ffn", "mxnorm_scales_bytes", "mxnorm_last_error")
+        m.set_library(MXNormError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        _binding_module = m
+    return _binding_module
 
 
-def _current(x):
-    """x's device index; the library launches on the current device, so
-    tensors of another one are refused."""
-    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
-    if dev < 0:
+def _launch(fn, x, stream, args):
+    """fn(*args, stream handle): on the current stream of x's device, or on
+    `stream`, inside which outputs and workspaces are then allocated -- memory
+    of that stream, so that the allocator orders its reuse after the kernels."""
+    if stream is None:
+        on_gpu = isinstance(x, torch.Tensor) and x.is_cuda
+        return fn(*args, torch._C._cuda_getCurrentRawStream(x.get_device()) if on_gpu else 0)
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-@contextlib.contextmanager
-def _on(stream, dev):
-    """The raw handle of the stream to launch on.  Outputs and workspaces are
-    allocated inside: memory of that stream, so that the allocator orders its
-    reuse after the kernels."""
+    dev = x.get_device()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream(dev)
     if stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     with torch.cuda.stream(stream):
-        yield stream.cuda_stream
-
-
-def _output(t, name, shape, dtype, like):
-    """A new tensor, or the caller's buffer checked against what will be written."""
-    if t is None:
-        return like.new_empty(shape, dtype=dtype)
-    _check_buffer(t, name, math.prod(shape) * dtype.itemsize, dtype, like.device)
-    return t
-
-
-def _workspace(t, nbytes, like):
-    if t is None:
-        return like.new_empty(max(nbytes, 16), dtype=torch.uint8)
-    if not isinstance(t, torch.Tensor):
-        raise ValueError("workspace must be a tensor")
-    _check_buffer(t, "workspace", nbytes, t.dtype, like.device)
-    return t
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+        return fn(*args, stream.cuda_stream)
 
 
 def layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
@@ -379,29 +353,7 @@ def layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, y=None, mean=None
     """Layer norm over the rows of x [T, D] (bf16, fp16 or fp32; any D and row
     stride): returns (y [T, D], mean fp32 [T], rstd fp32 [T]); the statistics
     are None with want_stats=False, unless buffers are given."""
-    dev = _current(x)
-    if stream is not None:
-        with _on(stream, dev) as s:
-            return _layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, dev, s)
-    return _layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, dev, torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, dev, stream):
-    dtype = x.dtype
-    if x.dim() != 2 or dtype not in DTYPE:
-        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
-    T, D = shape = x.shape
-    px = _input(x, "x", shape, dtype, dev, False)
-    pg = None if gamma is None else _input(gamma, "gamma", (D,), dtype, dev)
-    pb = None if beta is None else _input(beta, "beta", (D,), dtype, dev)
-    y = _output(y, "y", shape, dtype, x)
-    if want_stats or mean is not None:
-        mean = _output(mean, "mean", (T,), torch.float32, x)
-    if want_stats or rstd is not None:
-        rstd = _output(rstd, "rstd", (T,), torch.float32, x)
-    _check(lib().layernorm_fwd(px, pg, pb, y.data_ptr(), _addr(mean), _addr(rstd), T, D, _ld(x), eps, DTYPE[dtype],
-                               stream))
-    return y, mean, rstd
+    return _launch(_binding().layernorm_fwd, x, stream, (x, gamma, beta, eps, y, mean, rstd, want_stats))
 
 
 def layernorm_bwd_workspace_bytes(T: int, D: int, dtype=torch.bfloat16) -> int:
@@ -412,75 +364,22 @@ def layernorm_bwd(x, dy, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, wo
                   want_dgamma: bool = True, want_dbeta: bool = True, stream=None):
     """Layer norm's backward: returns (dx [T, D], dgamma [D] or None, dbeta [D]
     or None).  gamma may be None; there is then no dgamma."""
-    dev = _current(x)
-    args = (x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace, want_dgamma, want_dbeta, dev)
-    if stream is not None:
-        with _on(stream, dev) as s:
-            return _layernorm_bwd(*args, s)
-    return _layernorm_bwd(*args, torch._C._cuda_getCurrentRawStream(dev))
+    return _launch(_binding().layernorm_bwd, x, stream,
+                   (x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace, want_dgamma, want_dbeta))
 
 
-def _layernorm_bwd(x, dy, gamma, mean, rstd, dx, dgamma, dbeta, workspace, want_dgamma, want_dbeta, dev, stream):
-    dtype = x.dtype
-    if x.dim() != 2 or dtype not in DTYPE:
-        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
-    T, D = shape = x.shape
-    px = _input(x, "x", shape, dtype, dev, False)
-    py = _input(dy, "dy", shape, dtype, dev, False)
-    pg = None if gamma is None else _input(gamma, "gamma", (D,), dtype, dev)
-    pm = _input(mean, "mean", (T,), torch.float32, dev)
-    pr = _input(rstd, "rstd", (T,), torch.float32, dev)
-    dx = _output(dx, "dx", shape, dtype, x)
-    if dgamma is not None or (want_dgamma and gamma is not None):
-        dgamma = _output(dgamma, "dgamma", (D,), dtype, x)
-    if dbeta is not None or want_dbeta:
-        dbeta = _output(dbeta, "dbeta", (D,), dtype, x)
-    pw, nbytes = None, 0
-    if dgamma is not None or dbeta is not None:
-        workspace = _workspace(workspace, int(lib().layernorm_bwd_workspace_size(T, D, DTYPE[dtype])), x)
-        pw, nbytes = workspace.data_ptr(), workspace.nbytes
-    _check(lib().layernorm_bwd(px, py, pg, pm, pr, dx.data_ptr(), _addr(dgamma), _addr(dbeta), T, D, _ld(x), _ld(dy),
-                               DTYPE[dtype], pw, nbytes, stream))
-    return dx, dgamma, dbeta
-
-
-def _ffn_inputs(x, w_gate, w_up, act, dev):
-    """Checks the operands of the bf16 projections: ((x, w_gate, w_up), (T, D, F, ld_x, ld_w))."""
-    if act not in ACT:
-        raise ValueError(f"unknown activation {act!r}")
-    if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
-        raise ValueError("x must be [T, D] and the weights [F, D]")
-    T, D = x.shape
-    F = w_gate.shape[0]
-    ptrs = (_input(x, "x", (T, D), torch.bfloat16, dev, False),
-            _input(w_gate, "w_gate", (F, D), torch.bfloat16, dev, False),
-            _input(w_up, "w_up", (F, D), torch.bfloat16, dev, False))
-    ld_w = _ld(w_gate)
-    if ld_w != _ld(w_up):
-        raise ValueError("w_gate and w_up must have the same row stride")
-    return ptrs, (T, D, F, _ld(x), ld_w)
+def _choice(table, name, what):
+    if name not in table:
+        raise ValueError(f"unknown {what} {name!r}")
+    return table[name]
 
 
 def gated_ffn_fwd(x, w_gate, w_up, act: str = "silu", save: bool = False, h=None, gate=None, up=None, stream=None):
     """h = act(x w_gate^T) * (x w_up^T) in bf16: returns (h [T, F], gate, up).
     save: keep the projections [T, F] for gated_ffn_bwd (else None); act:
     "silu", "gelu" or "gelu_tanh"."""
-    dev = _current(x)
-    if stream is not None:
-        with _on(stream, dev) as s:
-            return _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, s)
-    return _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _gated_ffn_fwd(x, w_gate, w_up, act, save, h, gate, up, dev, stream):
-    ptrs, dims = _ffn_inputs(x, w_gate, w_up, act, dev)
-    shape = (dims[0], dims[2])
-    h = _output(h, "h", shape, torch.bfloat16, x)
-    if save or gate is not None or up is not None:
-        gate = _output(gate, "gate", shape, torch.bfloat16, x)
-        up = _output(up, "up", shape, torch.bfloat16, x)
-    _check(lib().gated_ffn_fwd(*ptrs, h.data_ptr(), _addr(gate), _addr(up), *dims, ACT[act], stream))
-    return h, gate, up
+    return _launch(_binding().gated_ffn_fwd, x, stream,
+                   (x, w_gate, w_up, _choice(ACT, act, "activation"), save, h, gate, up))
 
 
 def gated_ffn_bwd_workspace_bytes(T: int, D: int, F: int) -> int:
@@ -491,29 +390,9 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None, dw_
                   workspace=None, want_dx: bool = True, want_dw: bool = True, stream=None):
     """Backward of gated_ffn_fwd from the gate and up it kept: returns
     (dx [T, D], dw_gate [F, D], dw_up [F, D]), None where not wanted."""
-    dev = _current(x)
-    args = (dh, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, workspace, want_dx, want_dw, dev)
-    if stream is not None:
-        with _on(stream, dev) as s:
-            return _gated_ffn_bwd(*args, s)
-    return _gated_ffn_bwd(*args, torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act, dx, dw_gate, dw_up, workspace, want_dx, want_dw, dev, stream):
-    ptrs, dims = _ffn_inputs(x, w_gate, w_up, act, dev)
-    T, D, F = dims[:3]
-    ph = _input(dh, "dh", (T, F), torch.bfloat16, dev)
-    pg = _input(gate, "gate", (T, F), torch.bfloat16, dev)
-    pu = _input(up, "up", (T, F), torch.bfloat16, dev)
-    if want_dx or dx is not None:
-        dx = _output(dx, "dx", (T, D), torch.bfloat16, x)
-    if want_dw or dw_gate is not None or dw_up is not None:
-        dw_gate = _output(dw_gate, "dw_gate", (F, D), torch.bfloat16, x)
-        dw_up = _output(dw_up, "dw_up", (F, D), torch.bfloat16, x)
-    workspace = _workspace(workspace, gated_ffn_bwd_workspace_bytes(T, D, F), x)
-    _check(lib().gated_ffn_bwd(ph, *ptrs, pg, pu, _addr(dx), _addr(dw_gate), _addr(dw_up), *dims, ACT[act],
-                               workspace.data_ptr(), workspace.nbytes, stream))
-    return dx, dw_gate, dw_up
+    return _launch(_binding().gated_ffn_bwd, x, stream,
+                   (dh, x, w_gate, w_up, gate, up, _choice(ACT, act, "activation"), dx, dw_gate, dw_up, workspace,
+                    want_dx, want_dw))
 
 
 def mxfp8_gated_ffn(a_q, a_s, g_q, g_s, u_q, u_s, T: int, F: int, K: int, act: str = "silu", out: str = "bf16",
@@ -521,41 +400,9 @@ def mxfp8_gated_ffn(a_q, a_s, g_q, g_s, u_q, u_s, T: int, F: int, K: int, act: s
     """h = act(A Wg^T) * (A Wu^T) on MXFP8 operands (codes, and scales in the
     MMA layout): returns (h bf16 [T, F], None), or with out="e4m3" (codes
     uint8 [T, F], scales uint8), the A operand of the next mxfp8_gemm."""
-    dev = _current(a_q)
-    args = (a_q, a_s, g_q, g_s, u_q, u_s, T, F, K, act, out, int(scale_layout), h, h_s, dev)
-    if stream is not None:
-        with _on(stream, dev) as s:
-            return _mxfp8_gated_ffn(*args, s)
-    return _mxfp8_gated_ffn(*args, torch._C._cuda_getCurrentRawStream(dev))
-
-
-def _operand(t, name, nbytes, dev):
-    """A contiguous uint8 operand of at least nbytes bytes: its data pointer."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype is not torch.uint8 or not t.is_contiguous() or t.numel() < nbytes:
-        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {nbytes} bytes")
-    return t.data_ptr()
-
-
-def _mxfp8_gated_ffn(a_q, a_s, g_q, g_s, u_q, u_s, T, F, K, act, out, scale_layout, h, h_s, dev, stream):
-    if act not in ACT or out not in FFN_OUT:
-        raise ValueError(f"unknown activation {act!r} or output {out!r}")
-    s_t, s_f = scales_bytes(T, K, SCALES_MMA), scales_bytes(F, K, SCALES_MMA)
-    ptrs = (_operand(a_q, "a_q", T * K, dev), _operand(a_s, "a_s", s_t, dev), _operand(g_q, "g_q", F * K, dev),
-            _operand(g_s, "g_s", s_f, dev), _operand(u_q, "u_q", F * K, dev), _operand(u_s, "u_s", s_f, dev))
-    if out == "bf16":
-        h = _output(h, "h", (T, F), torch.bfloat16, a_q)
-        if h_s is not None:
-            raise ValueError("h_s is given for bf16 output")
-    else:
-        h = _output(h, "h", (T, F), torch.uint8, a_q)
-        n = scales_bytes(T, F, scale_layout)
-        _check_buffer(h_s, "h_s", n, torch.uint8, a_q.device)
-        if h_s is None:
-            h_s = (a_q.new_empty((T, F // 32)) if scale_layout == SCALES_ROWMAJOR else a_q.new_zeros(max(n, 1)))
-    _check(lib().mxfp8_gated_ffn(*ptrs, h.data_ptr(), _addr(h_s), T, F, K, ACT[act], FFN_OUT[out], scale_layout, stream))
-    return h, h_s
+    return _launch(_binding().mxfp8_gated_ffn, a_q, stream,
+                   (a_q, a_s, g_q, g_s, u_q, u_s, T, F, K, _choice(ACT, act, "activation"), _choice(FFN_OUT, out, "output"),
+                    scale_layout, h, h_s))
 
 
 def device_status(stream=None) -> int:
@@ -583,4 +430,4 @@ def algorithmic_bytes_fwd(T: int, D: int, gamma: bool = True, G_out: bool = True
     return T * D * 2 + T * D + T * (D // 32) + (2 * D if gamma else 0) + (4 * T if G_out else 0)
 
 
-__all__ = [n for n in dir() if not n.startswith("_") and n not in ("contextlib", "ctypes", "math", "os", "torch")]
+__all__ = [n for n in dir() if not n.startswith("_") and n not in ("ctypes", "importlib", "math", "os", "torch")]
