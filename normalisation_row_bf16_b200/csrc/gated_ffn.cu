@@ -445,123 +445,124 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
     };
     uint32_t it = 0, uses[2] = {0, 0};
     bool ok = true;
+    auto wait_full = [&](uint32_t acc) {
+      ok = mbar_wait_bounded(&S.acc_full[acc], uses[acc]++ & 1u, A.status) && !failed_flag(S);
+      tc_fence_after();
+      if (!ok && lane == 0) atomicOr(&S.failed, 1u);
+      return ok;
+    };
     for (int t = first; t < A.tiles && ok; t += step, ++it) {
       const TilePos q = tile_pos<PAIR>(A, t);
-      for (int a = 0; a < (PAIR ? q.halves : 1) && ok; ++a) {
-        const uint32_t acc = PAIR ? (uint32_t)a : (it & 1u);
-        const bool got = mbar_wait_bounded(&S.acc_full[acc], uses[acc]++ & 1u, A.status);
-        tc_fence_after();
-        if (!got || failed_flag(S)) {
-          if (lane == 0) atomicOr(&S.failed, 1u);
-          ok = false;
-          break;
-        }
-        const int row0 = q.m0 + a * 256 + (int)rank * 128 + quarter * 32;
-        const uint32_t ta = tmem + acc * 256u + ((uint32_t)(quarter * 32) << 16);
-        if constexpr (!PAIR) {
-          const int row = row0 + lane;
-          const bool live = row < A.M;
-          const int end = min(A.N, (q.nt + 1) * A.tile_n);
-          for (int c = half * 16; c < A.tile_n; c += 32) {
-            const int col = q.nt * A.tile_n + c;
-            uint32_t r[16], o[8];
-            tmem_ld16(ta + (uint32_t)c, r);
-            if constexpr (MODE == kGate) {
-              uint32_t u[16];
-              tmem_ld16(ta + (uint32_t)(A.tile_n + c), u);
-              tmem_ld16_fence(r, true);
-              tmem_ld16_fence(u, false);
-              gate_product(A.act, r, u, o);
-              if (live) {
-                store_cols16(A.out[0] + (int64_t)row * A.ld_out, col, end, o);
-                if (A.out[1]) {
-                  pack16(r, o);
-                  store_cols16(A.out[1] + (int64_t)row * A.ld_out, col, end, o);
-                  pack16(u, o);
-                  store_cols16(A.out[2] + (int64_t)row * A.ld_out, col, end, o);
-                }
+      const int row0 = q.m0 + (int)rank * 128 + quarter * 32;        // of the first accumulator; the second: 256 on
+      const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+      if constexpr (!PAIR) {
+        const uint32_t acc = it & 1u, ta = lanes + acc * 256u;
+        if (!wait_full(acc)) break;
+        const int row = row0 + lane;
+        const bool live = row < A.M;
+        const int end = min(A.N, (q.nt + 1) * A.tile_n);
+        for (int c = half * 16; c < A.tile_n; c += 32) {
+          const int col = q.nt * A.tile_n + c;
+          uint32_t r[16], o[8];
+          tmem_ld16(ta + (uint32_t)c, r);
+          if constexpr (MODE == kGate) {
+            uint32_t u[16];
+            tmem_ld16(ta + (uint32_t)(A.tile_n + c), u);
+            tmem_ld16_fence(r, true);
+            tmem_ld16_fence(u, false);
+            gate_product(A.act, r, u, o);
+            if (live) {
+              store_cols16(A.out[0] + (int64_t)row * A.ld_out, col, end, o);
+              if (A.out[1]) {
+                pack16(r, o);
+                store_cols16(A.out[1] + (int64_t)row * A.ld_out, col, end, o);
+                pack16(u, o);
+                store_cols16(A.out[2] + (int64_t)row * A.ld_out, col, end, o);
               }
+            }
+          } else {
+            tmem_ld16_fence(r, true);
+            if (MODE == kDx && A.partial) {
+              if (live) store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row) * A.N, col, end, r);
             } else {
-              tmem_ld16_fence(r, true);
-              if (MODE == kDx && A.partial) {
-                if (live) store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row) * A.N, col, end, r);
-                __syncwarp();
-                continue;
-              }
               pack16(r, o);
               if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, end, o);
             }
-            __syncwarp();                        // tcgen05.ld needs the warp converged
           }
-        } else if constexpr (MODE == kGate) {
-          // 64 features a warp: h, and gate and up when kept, packed in
-          // registers so that the accumulator goes back before the stores
-          const int col0 = q.nt * A.tile_n + half * 64;
-          uint32_t o[3][4][8];
+          __syncwarp();                          // tcgen05.ld needs the warp converged
+        }
+        hand_back(acc);
+      } else if (MODE == kDx && A.partial) {
+        for (int a = 0; a < q.halves; ++a) {
+          if (!wait_full((uint32_t)a)) break;
+          const int row = row0 + a * 256 + lane;
+          for (int c = half * 128; c < half * 128 + 128; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(lanes + (uint32_t)(a * 256 + c), r);
+            tmem_ld16_fence(r, true);
+            if (row < A.M)
+              store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row) * A.N, q.nt * A.tile_n + c, A.N, r);
+            __syncwarp();
+          }
+          hand_back((uint32_t)a);
+        }
+      } else {
+        // Boxes of 64 columns a warp: kGate h, gate and up of its 64 features, else two of its 128 columns.  An
+        // accumulator goes to registers, packed, and back to the MMA thread before the stores; in the backward, whose
+        // contractions can be short, both do (2048 rows: dw 398 -> 369 us; kGate has no registers for it).
+        constexpr int kBoxes = MODE == kGate ? 3 : 2, kHeld = MODE == kGate ? 1 : 2;
+        uint32_t o[kHeld][kBoxes][4][8];
+        const int n_box = MODE == kGate ? (A.out[1] ? 3 : 1) : 2;
+        auto drain = [&](int a) {
+          const uint32_t ta = lanes + (uint32_t)(a * 256 + half * (MODE == kGate ? 64 : 128));
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t r[16], u[16];
-            tmem_ld16(ta + (uint32_t)(half * 64 + 16 * c), r);
-            tmem_ld16(ta + (uint32_t)(128 + half * 64 + 16 * c), u);
+            tmem_ld16(ta + 16u * c, r);
+            tmem_ld16(ta + (MODE == kGate ? 128u : 64u) + 16u * c, u);
             tmem_ld16_fence(r, true);
             tmem_ld16_fence(u, false);
-            gate_product(A.act, r, u, o[0][c]);
-            pack16(r, o[1][c]);
-            pack16(u, o[2][c]);
+            if constexpr (MODE == kGate) {
+              gate_product(A.act, r, u, o[a % kHeld][0][c]);
+              pack16(r, o[a % kHeld][kBoxes - 2][c]);
+              pack16(u, o[a % kHeld][kBoxes - 1][c]);
+            } else {
+              pack16(r, o[a % kHeld][0][c]);
+              pack16(u, o[a % kHeld][1][c]);
+            }
             __syncwarp();
           }
-          hand_back(acc);
-          const int n_out = A.out[1] ? 3 : 1;
+          hand_back((uint32_t)a);
+        };
+        auto store = [&](int a, int b) {
+          const int row = row0 + a * 256;
+          const int col = q.nt * A.tile_n + half * (MODE == kGate ? 64 : 128) + (MODE == kGate ? 0 : b * 64);
+          if (lane == 0) bulk_wait_read_all();   // the box before has left
+          __syncwarp();
 #pragma unroll
-          for (int b = 0; b < 3; ++b) {
-            if (b >= n_out) break;
-            if (lane == 0) bulk_wait_read_all();   // the box before has left
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) put2(2 * c, o[b][c]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && row0 < A.M && col0 < A.N) {
-              tma_store_2d(&A.c[b], box, col0, row0);
-              bulk_commit();
-            }
+          for (int c = 0; c < 4; ++c) put2(2 * c, o[a % kHeld][b][c]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row < A.M && col < A.N) {
+            tma_store_2d(&A.c[MODE == kGate ? b : (MODE == kDw ? q.p : 0)], box, col, row);
+            bulk_commit();
           }
-        } else {
-          // 128 columns a warp, in two boxes through one buffer
+        };
+        auto store_all = [&](int a) {
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int col0 = q.nt * A.tile_n + half * 128 + v * 64;
-            uint32_t r[4][16], o[8];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld16(ta + (uint32_t)(half * 128 + v * 64 + 16 * c), r[c]);
-            tmem_ld16_fence(r[0], true);
-#pragma unroll
-            for (int c = 1; c < 4; ++c) tmem_ld16_fence(r[c], false);
-            if (MODE == kDx && A.partial) {
-              if (row0 + lane < A.M) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row0 + lane) * A.N, col0 + 16 * c, A.N, r[c]);
-              }
-              __syncwarp();
-              continue;
-            }
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              pack16(r[c], o);
-              put2(2 * c, o);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && row0 < A.M && col0 < A.N) {
-              tma_store_2d(&A.c[MODE == kDw ? q.p : 0], box, col0, row0);
-              bulk_commit();
-            }
-          }
+          for (int b = 0; b < kBoxes; ++b)
+            if (b < n_box) store(a, b);
+        };
+        if (!wait_full(0)) break;
+        drain(0);
+        if constexpr (MODE == kGate) store_all(0);
+        else store(0, 0);
+        if (q.halves == 2) {
+          if (!wait_full(1)) break;
+          drain(1);
         }
-        if constexpr (!(PAIR && MODE == kGate)) hand_back(acc);
+        if constexpr (MODE != kGate) store(0, 1);
+        if (q.halves == 2) store_all(1);
       }
     }
     if (PAIR && lane == 0) bulk_wait_read_all(); // before the CTA's shared memory goes
