@@ -121,11 +121,20 @@ __device__ __forceinline__ void store_mxfp8(const Args& A, int row, int col, con
 // share 256 x 256 tiles; each loads 128 rows of A with their scale atom, one of
 // the two weights' 128 rows (CTA 0 gate, CTA 1 up) and both weights' atoms, and
 // CTA 0 issues tcgen05.mma.cta_group::2 for both: a third fewer operand bytes
-// from L2, which bound the 128 x 256 tiles (11.4 GB in 855 us at 8192 x 14336 x
-// 4096).  Single CTAs take the calls of few rows: a stage then holds only the
-// rows of A there are (in eights), so that more stages of weights are in
-// flight; the MMA's 128-row window runs on into the bytes behind them, which
-// only reach accumulator rows that are never stored.
+// from L2 than 128 x 256 tiles.  At 8192 x 4096 x 14336 pairs run 807 us (923
+// back to back, under the power limit), single CTAs 851 (997).
+// What bounds it: a stage's turn from the commit that frees it to the MMA on
+// its new contents takes about 2.5 us, so the 6 stages pass at 0.45 us each
+// where the MMAs alone would take 0.38, and a tile's change of accumulator
+// costs 1.2 us more -- 256 columns and the scales leave tensor memory no room
+// for a second one.  The MMA thread's own instructions count too: descriptors
+// built per stage and two commits a stage took 882 us.  Built and measured, not
+// kept: gate and up as two N = 128 MMAs over three rotating accumulators (1073
+// us), polling waits in place of sleeping ones (895 us).
+// Single CTAs take the calls of few rows: a stage then holds only the rows of A
+// there are (in eights), so that more stages of weights are in flight (16 rows:
+// 34.4 -> 23.6 us); the MMA's 128-row window runs on into the bytes behind
+// them, which only reach accumulator rows that are never stored.
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_constant__ Args A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];

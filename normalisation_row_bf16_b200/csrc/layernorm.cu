@@ -8,7 +8,12 @@
 //   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
 // Arithmetic and every sum are fp32; y, dx, dgamma and dbeta are rounded once.
 // Both passes are bound by HBM: 2 (forward) and 3 (backward) elements move per
-// element of x, with about 8 and 14 flops each.
+// element of x, with about 8 and 14 flops each.  At 8192 x 4096 bf16 the forward
+// runs 24.0 us (5.6 TB/s, 0.87 of a measured copy) and the backward 40.4 us with
+// the reduction of dgamma and dbeta (5.0 TB/s, 0.77); fp32 45.9 and 68.8 us (0.90
+// and 0.91).  16-bit elements cost twice the instructions a byte, so the work is
+// in packed fp32 pairs on rows held in registers, few reductions, and copies
+// that need no thread.
 #include "layernorm.h"
 
 #include <cuda_fp16.h>
@@ -532,6 +537,10 @@ __host__ __device__ constexpr int ln_bwd_threads(bool keep) { return keep ? 384 
 // packed, between the passes, and its stage is refilled behind the barrier of
 // the reduction; otherwise the second pass reads the stage again and the
 // barrier frees the row before (a ring of one stage has a barrier of its own).
+// Measured at 8192 x 4096 bf16: 60.8 us with scalar arithmetic, 60.1 with a pass
+// of row sums by warps and one of columns by all threads (32 instructions an
+// element), 47.6 as here, 40.4 once the groups' column sums were folded side by
+// side instead of in turn with conflicting banks.
 // V = 16 / sizeof(T) elements a chunk, or 1 when rows do not all start on
 // 16-byte boundaries.  gamma lies in shared memory as fp32, for V = 8 in two
 // planes of four columns a chunk, so that lanes read 16 consecutive bytes.
