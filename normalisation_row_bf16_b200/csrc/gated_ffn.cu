@@ -29,7 +29,7 @@ namespace {
 
 enum Mode { kGate, kDx, kDw };
 
-constexpr int kTileK = 64;                       // contraction elements (128 bytes) per stage
+constexpr int kTileK = 64;                       // contraction elements (128 bytes) of a k-block
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;                     // 4 lane quarters x 2 column halves
 constexpr int kThreads = 64 + 32 * kEpiWarps;    // producer warp, MMA warp, epilogue warps
@@ -49,13 +49,13 @@ struct Args {
   int m_tiles, n_tiles;  // tiles of one problem (pairs: whole 512-row tiles)
   int tiles, whole;      // work units of all problems; pairs: those that are whole 512-row tiles
   int m_halves;          // pairs: 256-row halves of one problem
-  int n_k, n_k0;         // K stages of a tile, and of its first segment (kDx)
+  int n_k, n_k0;         // k-blocks of a tile, and of its first segment (kDx)
   int tile_n;            // output columns of a tile (kGate: features, each with a gate and an up column)
   int acc_n;             // accumulator columns: 2 * tile_n (kGate) or tile_n
   int act;
   int a_rows;            // rows of A that a stage of a single CTA holds
-  int stages;
-  uint32_t stage_bytes;
+  int stages, group;     // ring depth, k-blocks (kTileK elements) a stage holds
+  uint32_t stage_bytes, block_bytes;
 };
 
 struct Barriers {
@@ -176,7 +176,7 @@ __device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
   return q;
 }
 
-// K stages [k_lo, k_hi) of problem p.  kDx deals its contraction to `problems`
+// k-blocks [k_lo, k_hi) of problem p.  kDx deals its contraction to `problems`
 // partial products of the same output.
 template <int MODE>
 __device__ __forceinline__ int k_lo(const Args& A, int p) {
@@ -299,90 +299,101 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
   griddep_launch_dependents();
 
   uint32_t n_issued = 0;
+  const int G = PAIR ? 1 : A.group;
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- producer
-      uint32_t s = 0, ph = 1;
-      bool ok = true;
-      for (int t = first; t < A.tiles && ok; t += step) {
-        const TilePos q = tile_pos<PAIR>(A, t);
-        // bytes of a stage: tiles of one half leave A's second block out
-        const uint32_t bytes = PAIR && q.halves == 1 ? A.stage_bytes - kABytes : A.stage_bytes;
-        const int k_end = k_hi<MODE>(A, q.p);
-        for (int kb = k_lo<MODE>(A, q.p); kb < k_end; ++kb) {
-          if (!mbar_wait_bounded(&S.empty[s], ph, A.status) || failed_flag(S)) {
-            atomicOr(&S.failed, 1u);
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes;
-          uint8_t* sb = sa + b_off;
-          const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * bytes : bytes);
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    uint32_t s = 0, ph = 1;
+    bool ok = true;
+    for (int t = first; t < A.tiles && ok; t += step) {
+      const TilePos q = tile_pos<PAIR>(A, t);
+      // tiles of one half leave A's second block out
+      const uint32_t block_bytes = PAIR && q.halves == 1 ? A.block_bytes - kABytes : A.block_bytes;
+      const int k_end = k_hi<MODE>(A, q.p), blocks = PAIR ? q.halves : 1;
+      if (__any_sync(0xFFFFFFFFu, failed_flag(S))) break;
+      for (int kb0 = k_lo<MODE>(A, q.p); kb0 < k_end; kb0 += G) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.empty[s], ph, A.status));
+        if (!ok) break;
+        const int n = PAIR ? 1 : min(G, k_end - kb0);
+        const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
+        if (leader) {
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * block_bytes : n * block_bytes);
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) { tma_load<PAIR>(dst, map, x, y, bar); };
-          const int blocks = PAIR ? q.halves : 1;
-          if constexpr (MODE == kGate) {
-            for (int h = 0; h < blocks; ++h) load(sa + h * kABytes, &A.a[0], kb * kTileK, q.m0 + h * 256 + (int)rank * 128);
-            if constexpr (PAIR) {
-              load(sb, &A.b[rank], kb * kTileK, q.nt * A.tile_n);
-            } else {
-              load(sb, &A.b[0], kb * kTileK, q.nt * A.tile_n);
-              load(sb + A.tile_n * 128, &A.b[1], kb * kTileK, q.nt * A.tile_n);
-            }
-          } else {
-            const int n0 = q.nt * A.tile_n + (PAIR ? (int)rank * 128 : 0), nb = PAIR ? 128 : A.tile_n;
-            const int seg = MODE == kDx && kb >= A.n_k0, k0 = (kb - seg * A.n_k0) * kTileK;
-            for (int h = 0; h < blocks; ++h) {
-              const int m = q.m0 + h * 256 + (int)rank * 128;
-              if constexpr (MODE == kDx) {
-                load(sa + h * kABytes, &A.a[seg], k0, m);
+          for (int g = 0; g < n; ++g) {
+            const int kb = kb0 + g;
+            uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes + (size_t)g * A.block_bytes;
+            uint8_t* sb = sa + b_off;
+            if constexpr (MODE == kGate) {
+              for (int h = 0; h < blocks; ++h) load(sa + h * kABytes, &A.a[0], kb * kTileK, q.m0 + h * 256 + (int)rank * 128);
+              if constexpr (PAIR) {
+                load(sb, &A.b[rank], kb * kTileK, q.nt * A.tile_n);
               } else {
-                load(sa + h * kABytes, &A.a[q.p], m, k0);
-                load(sa + h * kABytes + kABytes / 2, &A.a[q.p], m + 64, k0);
+                load(sb, &A.b[0], kb * kTileK, q.nt * A.tile_n);
+                load(sb + A.tile_n * 128, &A.b[1], kb * kTileK, q.nt * A.tile_n);
               }
+            } else {
+              const int n0 = q.nt * A.tile_n + (PAIR ? (int)rank * 128 : 0), nb = PAIR ? 128 : A.tile_n;
+              const int seg = MODE == kDx && kb >= A.n_k0, k0 = (kb - seg * A.n_k0) * kTileK;
+              for (int h = 0; h < blocks; ++h) {
+                const int m = q.m0 + h * 256 + (int)rank * 128;
+                if constexpr (MODE == kDx) {
+                  load(sa + h * kABytes, &A.a[seg], k0, m);
+                } else {
+                  load(sa + h * kABytes, &A.a[q.p], m, k0);
+                  load(sa + h * kABytes + kABytes / 2, &A.a[q.p], m + 64, k0);
+                }
+              }
+              for (int c = 0; c < nb; c += 64) load(sb + c * 128, &A.b[seg], n0 + c, k0);
             }
-            for (int c = 0; c < nb; c += 64) load(sb + c * 128, &A.b[seg], n0 + c, k0);
           }
-          ++n_issued;
-          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
         }
+        __syncwarp();
+        ++n_issued;
+        if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
       }
     }
+    if (!ok && leader) atomicOr(&S.failed, 1u);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------ MMA (of a pair: CTA 0)
+      const bool leader = elect_one();
       uint32_t s = 0, ph = 0, it = 0, uses[2] = {0, 0};
       bool ok = true;
       const uint32_t idesc = instr_desc(PAIR ? 256 : 128, A.acc_n, kAmn, kBmn);
       auto commit = [&](uint64_t* bar) {         // to both CTAs of a pair
-        if constexpr (PAIR) tc_commit_both(smem_u32(bar));
-        else tc_commit(bar);
+        if (leader) {
+          if constexpr (PAIR) tc_commit_both(smem_u32(bar));
+          else tc_commit(bar);
+        }
+        __syncwarp();
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && (!mbar_wait_bounded(bar, parity, A.status) || failed_flag(S))) {
-          atomicOr(&S.failed, 1u);
-          ok = false;
-        }
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, A.status));
         tc_fence_after();
       };
-      // One stage into accumulator `acc`, from the h-th block of A.
-      auto mma_stage = [&](uint32_t stage, int h, uint32_t acc, bool first_k) {
-        const uint32_t a0 = smem_u32(smem_raw) + stage * A.stage_bytes + (uint32_t)h * kABytes;
-        const uint32_t b0 = smem_u32(smem_raw) + stage * A.stage_bytes + b_off;
+      // One k-block at `at` (bytes into the ring, >> 4) into accumulator `acc`, from the h-th block of A.
+      const uint64_t a_desc = op_desc(smem_u32(smem_raw), 0, kAmn), b_desc = op_desc(smem_u32(smem_raw) + b_off, 0, kBmn);
+      auto mma_block = [&](uint32_t at, int h, uint32_t acc, bool first_k) {
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kTileK / 16; ++k)
-          mma_bf16<PAIR>(tmem + acc * 256u, op_desc(a0, k, kAmn), op_desc(b0, k, kBmn), idesc, (!first_k || k > 0) ? 1u : 0u);
+          for (int k = 0; k < kTileK / 16; ++k)
+            mma_bf16<PAIR>(tmem + acc * 256u, a_desc + (at + (uint32_t)h * (kABytes >> 4) + (kAmn ? 128u : 2u) * k),
+                           b_desc + (at + (kBmn ? 128u : 2u) * k), idesc, (!first_k || k > 0) ? 1u : 0u);
+        }
       };
+      const uint32_t stage4 = A.stage_bytes >> 4, block4 = A.block_bytes >> 4;
       for (int t = first; t < A.tiles && ok; t += step, ++it) {
         const TilePos q = tile_pos<PAIR>(A, t);
         const int n_k = k_hi<MODE>(A, q.p) - k_lo<MODE>(A, q.p);
+        if (__any_sync(0xFFFFFFFFu, failed_flag(S))) ok = false;
         if constexpr (!PAIR) {
           const uint32_t acc = it & 1u;
           wait(&S.acc_empty[acc], (uses[acc]++ & 1u) ^ 1u);
-          for (int kb = 0; kb < n_k && ok; ++kb) {
+          for (int kb = 0; kb < n_k && ok; kb += G) {
             wait(&S.full[s], ph);
             if (!ok) break;
-            mma_stage(s, 0, acc, kb == 0);
+            const int n = min(G, n_k - kb);
+            for (int g = 0; g < n; ++g) mma_block(s * stage4 + g * block4, 0, acc, kb + g == 0);
             commit(&S.empty[s]);
             if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
           }
@@ -395,13 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           for (int kb = 0; kb < lead && ok; ++kb) {
             wait(&S.full[s], ph);
             if (!ok) break;
-            mma_stage(s, 0, 0, kb == 0);
+            mma_block(s * stage4, 0, 0, kb == 0);
             if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
           }
           if (halves == 2) {
             wait(&S.acc_empty[1], (uses[1]++ & 1u) ^ 1u);
             for (int kb = 0; kb < lead && ok; ++kb) {
-              mma_stage(s1, 1, 1, kb == 0);
+              mma_block(s1 * stage4, 1, 1, kb == 0);
               commit(&S.empty[s1]);
               if (++s1 == (uint32_t)A.stages) s1 = 0;
             }
@@ -409,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           for (int kb = lead; kb < n_k && ok; ++kb) {
             wait(&S.full[s], ph);
             if (!ok) break;
-            mma_stage(s, 0, 0, kb == 0);
-            if (halves == 2) mma_stage(s, 1, 1, kb == 0);
+            mma_block(s * stage4, 0, 0, kb == 0);
+            if (halves == 2) mma_block(s * stage4, 1, 1, kb == 0);
             commit(&S.empty[s]);
             if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
           }
@@ -418,8 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           if (ok && halves == 2) commit(&S.acc_full[1]);
         }
       }
-      if constexpr (PAIR) tc_commit_pair(smem_u32(&S.mma_done));
-      else tc_commit(&S.mma_done);
+      if (leader) {
+        if (!ok) atomicOr(&S.failed, 1u);
+        if constexpr (PAIR) tc_commit_pair(smem_u32(&S.mma_done));
+        else tc_commit(&S.mma_done);
+      }
+      __syncwarp();
       if (!ok) {                                 // wake the epilogues; they see the failure or time out
         commit(&S.acc_full[0]);
         commit(&S.acc_full[1]);
@@ -763,16 +778,25 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   A.tiles = (int)tiles;
   A.acc_n = mode == kGate ? 2 * A.tile_n : A.tile_n;
   if (L->pair) {
-    A.stage_bytes = kPairStage;
+    A.stage_bytes = A.block_bytes = kPairStage;
+    A.group = 1;
     A.stages = kPairStages;
     L->smem = kPairSmem;
     L->grid = 2 * (A.tiles < pairs ? A.tiles : pairs);
   } else {
-    A.stage_bytes = (uint32_t)(A.a_rows + A.acc_n) * 128u;
+    // Small tiles put up to four k-blocks in a stage, 48 KiB in all: a stage's
+    // waits and commit cost as much as those tiles' MMAs (7 x 2424 x 640: 13.9 ->
+    // 8.6 us, 100 x 4096 x 4096 23.0 -> 17.8).
+    A.block_bytes = (uint32_t)(A.a_rows + A.acc_n) * 128u;
+    A.group = (int)(49152 / A.block_bytes);
+    A.group = A.group < 1 ? 1 : (A.group > 4 ? 4 : A.group);
+    A.stage_bytes = A.group * A.block_bytes;
     A.stages = (int)(kSmemCap / A.stage_bytes);
     if (A.stages > kMaxStages) A.stages = kMaxStages;
+    // the last block's window of 128 rows of A lies in the shared memory too
+    while ((size_t)A.stages * A.stage_bytes - A.block_bytes + kABytes > kSmemCap) --A.stages;
     L->smem = (size_t)A.stages * A.stage_bytes + sizeof(Barriers);
-    const size_t window = (size_t)(A.stages - 1) * A.stage_bytes + kABytes;    // the last stage's 128 rows of A
+    const size_t window = (size_t)A.stages * A.stage_bytes - A.block_bytes + kABytes;
     if (L->smem < window) L->smem = window;
     L->grid = A.tiles < sms ? A.tiles : sms;
   }

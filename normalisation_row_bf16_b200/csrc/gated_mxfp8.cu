@@ -176,25 +176,24 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
 
   uint32_t n_issued = 0;
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- producer
-      uint32_t s = 0, ph = 1;
-      bool ok = true;
-      // bytes a CTA brings into a stage
-      const uint32_t bytes = (PAIR ? 2 * kRows128 : b_off + 2 * kRows128) + 3 * kAtom;
-      for (int t = first; t < tiles && ok; t += step) {
-        int mt, nt;
-        tile_pos(A, t, &mt, &nt);
-        const int mb = PAIR ? 2 * mt + (int)rank : mt;           // this CTA's 128-row block of A
-        for (int kb = 0; kb < n_k; ++kb) {
-          if (!mbar_wait_bounded(&S.empty[s], ph, A.status) || failed_flag(S)) {
-            atomicOr(&S.failed, 1u);
-            ok = false;
-            break;
-          }
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    uint32_t s = 0, ph = 1;
+    bool ok = true;
+    // bytes a CTA brings into a stage
+    const uint32_t bytes = (PAIR ? 2 * kRows128 : b_off + 2 * kRows128) + 3 * kAtom;
+    for (int t = first; t < tiles && ok; t += step) {
+      if (__any_sync(0xFFFFFFFFu, failed_flag(S))) break;
+      int mt, nt;
+      tile_pos(A, t, &mt, &nt);
+      const int mb = PAIR ? 2 * mt + (int)rank : mt;             // this CTA's 128-row block of A
+      for (int kb = 0; kb < n_k; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.empty[s], ph, A.status));
+        if (!ok) break;
+        const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
+        if (leader) {
           uint8_t* sa = smem_raw + (size_t)s * A.stage_bytes;
           uint8_t* sf = sa + A.sf_off;
-          const uint32_t bar = PAIR ? cluster_addr(&S.full[s], 0) : smem_u32(&S.full[s]);
           if (rank == 0) mbar_arrive_expect_tx(&S.full[s], PAIR ? 2 * bytes : bytes);
           tma_load<PAIR>(sa, &A.a, kb * kTileK, mb * 128, bar);
           if constexpr (PAIR) {
@@ -213,53 +212,60 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
             bulk_g2s_plain(sf + kAtom, A.w_s[0] + ((size_t)nt * n_k + kb) * kAtom, kAtom, full);
             bulk_g2s_plain(sf + 2 * kAtom, A.w_s[1] + ((size_t)nt * n_k + kb) * kAtom, kAtom, full);
           }
-          ++n_issued;
-          if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
         }
+        __syncwarp();
+        ++n_issued;
+        if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
       }
     }
+    if (!ok && leader) atomicOr(&S.failed, 1u);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------ MMA (of a pair: CTA 0)
+      const bool leader = elect_one();
       uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
       auto commit = [&](uint64_t* bar) {         // to both CTAs of a pair
-        if constexpr (PAIR) tc_commit_both(smem_u32(bar));
-        else tc_commit(bar);
+        if (leader) {
+          if constexpr (PAIR) tc_commit_both(smem_u32(bar));
+          else tc_commit(bar);
+        }
+        __syncwarp();
       };
-      const uint32_t base = smem_u32(smem_raw);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, A.status));
+        tc_fence_after();
+      };
+      const uint32_t base = smem_u32(smem_raw), stage4 = A.stage_bytes >> 4;
       const uint64_t a_desc = smem_desc(base, 16, 1024, 2), b_desc = smem_desc(base + b_off, 16, 1024, 2),
                      sf_desc = smem_desc(base + A.sf_off, 0, 128, 0);
       for (int t = first; t < tiles && ok; t += step, ++it) {
-        if (!mbar_wait_bounded(&S.acc_empty, (it & 1u) ^ 1u, A.status) || failed_flag(S)) {
-          atomicOr(&S.failed, 1u);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int kb = 0; kb < n_k; ++kb) {
-          if (!mbar_wait_bounded(&S.full[s], ph, A.status)) {
-            atomicOr(&S.failed, 1u);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (__any_sync(0xFFFFFFFFu, failed_flag(S))) ok = false;
+        wait(&S.acc_empty, (it & 1u) ^ 1u);
+        for (int kb = 0; kb < n_k && ok; ++kb) {
+          wait(&S.full[s], ph);
+          if (!ok) break;
           // descriptors: the start address (>> 4) is the low field
-          const uint64_t at = (uint64_t)(s * (A.stage_bytes >> 4));
-          const uint32_t sfa = tmem + kSfCol0 + s * 12u, sfb = sfa + 4u;
+          const uint32_t at = s * stage4, sfa = tmem + kSfCol0 + s * 12u, sfb = sfa + 4u;
+          if (leader) {
 #pragma unroll
-          for (int j = 0; j < 3; ++j) tmem_cp_sf<PAIR>(sfa + 4u * j, sf_desc + at + j * (kAtom >> 4));
+            for (int j = 0; j < 3; ++j) tmem_cp_sf<PAIR>(sfa + 4u * j, sf_desc + (at + j * (kAtom >> 4)));
 #pragma unroll
-          for (int k = 0; k < kTileK / 32; ++k)
-            mma_mxf8<PAIR>(tmem, a_desc + at + 2 * k, b_desc + at + 2 * k, instr_desc(PAIR ? 256 : 128, (uint32_t)k),
-                           sfa | ((uint32_t)k << 30), sfb | ((uint32_t)k << 30), (kb > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kTileK / 32; ++k)
+              mma_mxf8<PAIR>(tmem, a_desc + (at + 2 * k), b_desc + (at + 2 * k), instr_desc(PAIR ? 256 : 128, (uint32_t)k),
+                             sfa | ((uint32_t)k << 30), sfb | ((uint32_t)k << 30), (kb > 0 || k > 0) ? 1u : 0u);
+          }
           commit(&S.empty[s]);
           if (++s == (uint32_t)A.stages) { s = 0; ph ^= 1u; }
         }
         if (ok) commit(&S.acc_full);
       }
-      if constexpr (PAIR) tc_commit_pair(smem_u32(&S.mma_done));
-      else tc_commit(&S.mma_done);
+      if (leader) {
+        if (!ok) atomicOr(&S.failed, 1u);
+        if constexpr (PAIR) tc_commit_pair(smem_u32(&S.mma_done));
+        else tc_commit(&S.mma_done);
+      }
+      __syncwarp();
       if (!ok) commit(&S.acc_full);              // wake the epilogues; they see the failure or time out
     }
   } else {

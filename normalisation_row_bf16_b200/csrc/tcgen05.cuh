@@ -84,6 +84,20 @@ __device__ __forceinline__ void tmem_ld_fence(uint32_t (&r)[32], bool wait) {
 #undef MXN_R32
 }
 
+// True in one lane of a converged warp.  A role's warp runs its loop as a whole
+// and guards only the instructions that one thread issues: loop state then stays
+// warp-uniform, and the operands of TMA and tcgen05 instructions, which sit in
+// uniform registers, need no move from one thread's registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
