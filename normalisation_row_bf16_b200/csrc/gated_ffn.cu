@@ -708,12 +708,17 @@ const void* kernel_of(int mode, bool pair) {
 // false when the tiles outnumber an int.
 //
 // The shape with the least estimated time, from figures measured on B200: a
-// single CTA's K stage takes as long as its bytes at 90 GB/s an SM, and a
-// twelfth of the 2.5 us a ring takes around at least; a pair's 0.46 us for a
-// 256-row half and 0.77 for a whole tile; a tile 2.5 to 3 us more; and all
-// operands come from HBM once.  kDx may deal the contraction to up to 8 partial
-// products, which another kernel adds up (3 us and their bytes at 6 TB/s):
-// without it 333 x 1032 x 2744 took 25 us on 51 of 148 SMs.
+// single CTA's k-block takes as long as its bytes at 110 GB/s an SM (140 over
+// one or two rounds of tiles, 60 where they come from HBM), 0.12 us at least; a
+// pair's 0.40 us for a 256-row half and 0.66 for a whole tile; a tile 1 us more
+// on single CTAs, whose epilogue overlaps (3 where the contraction is the short
+// one, over the rows), and 4.5 on pairs, 6.5 with the activation; and all
+// operands come from HBM once.  So pairs win
+// where there are several rounds of tiles (4096 x 2048 x 5632 forward 130 us,
+// 146 on single CTAs; 1000 x 1024 x 2816 19.1 and 15.9).  kDx may deal the
+// contraction to up to 8 partial products, which another kernel adds up (3 us
+// and their bytes at 6 TB/s): without it 333 x 1032 x 2744 took 25 us on 51 of
+// 148 SMs.
 bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   constexpr uint32_t kPairStage = 3 * kABytes;
   constexpr int kPairStages = (int)((kSmemCap - kEpiWarps * kBoxBytes) / kPairStage);
@@ -740,10 +745,11 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
       const int64_t tiles = (int64_t)cdiv(A.M, 128) * cdiv(A.N, w) * probs, rounds = (tiles + sms - 1) / sms;
       // the second operand streams from HBM where only one row of tiles reads it
       const bool cold = A.M <= 128;
-      double kb = (A.a_rows / 90e3 + (mode == kGate ? 2 * w : w) / (cold ? 60e3 : 90e3)) * 128;
-      if (kb < 2.5 / kMaxStages) kb = 2.5 / kMaxStages;
+      const double rate = rounds <= 2 ? 140e3 : 110e3;
+      double kb = (A.a_rows / rate + (mode == kGate ? 2 * w : w) / (cold ? 60e3 : rate)) * 128;
+      if (kb < 0.12) kb = 0.12;
       const double stream = rounds * nk * kb;
-      if (better((stream > hbm ? stream : hbm) + rounds * 2.5 + sum)) {
+      if (better((stream > hbm ? stream : hbm) + 2.5 + rounds * (mode == kDw ? 3.0 * w / 256 : 1.0) + sum)) {
         L->pair = false;
         A.tile_n = w;
         A.problems = probs;
@@ -752,7 +758,7 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
     if (pairs > 0) {
       const int64_t n_tiles = (int64_t)cdiv(A.N, widest) * probs, halves = cdiv(A.M, 256);
       const int64_t whole = halves / 2 * n_tiles, odd = (halves & 1) * n_tiles, rest = whole % pairs;
-      const double t1 = nk * 0.46 + 3.0, t2 = nk * 0.77 + 3.0;
+      const double end = mode == kGate ? 6.5 : 4.5, t1 = nk * 0.40 + end, t2 = nk * 0.66 + end;
       const double us = 2 * rest + odd <= pairs
                             ? (double)(whole / pairs) * t2 + (rest || odd ? t1 : 0.0)
                             : (double)((whole + pairs - 1) / pairs) * t2 + (double)((odd + pairs - 1) / pairs) * t1;
