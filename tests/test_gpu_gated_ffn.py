@@ -450,3 +450,72 @@ def test_serving_chain():
     ref = hv @ dv.t()
     err = acc(F) * (hv.abs() @ dv.abs().t())
     assert ((y.double() - ref).abs() <= half_step(BF, ref.abs() + err) + err).all()
+
+
+def test_offsets_past_32_bits():
+    """Rows behind the 2^31st element of h, forward and backward."""
+    T, D, F = 150100, 64, 14336
+    x, wg, wu = inputs(T, D, F)
+    h, _, _ = ops.gated_ffn_fwd(x, wg, wu)
+    at = 2 ** 31 // F - 2
+    for r in (slice(at, at + 5), slice(T - 3, T)):
+        check_fwd(x[r], wg, wu, "silu", h[r])
+    gate = h
+    dx, dwg, dwu = ops.gated_ffn_bwd(h, x, wg, wu, gate, gate, want_dw=False)
+    for r in (slice(at, at + 5), slice(T - 3, T)):
+        check_bwd(h[r], x[r], wg, wu, gate[r], gate[r], "silu", dx[r], None, None)
+
+
+@pytest.mark.parametrize("T,D,F", [(700, 512, 1032), (4096, 256, 2048)])
+def test_two_calls_at_once(T, D, F):
+    """Calls on two streams do not disturb one another: small tiles and pairs of CTAs."""
+    sets = [(*inputs(T, D, F, seed=s), rand((T, F), s + 50, 0.1)) for s in (1, 7)]
+
+    def step(x, wg, wu, dh, stream=None):
+        h, gate, up = ops.gated_ffn_fwd(x, wg, wu, save=True, stream=stream)
+        return (h, *ops.gated_ffn_bwd(dh, x, wg, wu, gate, up, stream=stream))
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(6):
+        got = [step(*s, stream=st) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert ops.device_status() == ops.MXN_OK
+
+
+# Shapes that reach every plan of the products: one and several rounds of single CTAs and of pairs, whole 512-row tiles,
+# halves and the odd half, split contractions.
+PLAN_SHAPES = [(257, 512, 4096), (513, 256, 1024), (768, 4096, 2048), (1281, 1536, 4096), (2300, 1024, 4104), (5000, 512, 3000)]
+
+
+@pytest.mark.parametrize("T,D,F", PLAN_SHAPES)
+def test_plans(T, D, F):
+    x, wg, wu = inputs(T, D, F, seed=T)
+    h, gate, up = ops.gated_ffn_fwd(x, wg, wu, act="gelu", save=True)
+    check_fwd(x, wg, wu, "gelu", h, gate, up)
+    dh = rand((T, F), 5, 0.1)
+    check_bwd(dh, x, wg, wu, gate, up, "gelu", *ops.gated_ffn_bwd(dh, x, wg, wu, gate, up, act="gelu"))
+    assert ops.device_status() == ops.MXN_OK
+
+
+@pytest.mark.parametrize("T,F,K", [(257, 1024, 512), (1000, 4096, 256), (2300, 3104, 384)])
+def test_mxfp8_plans(T, F, K):
+    (aq, as_, av), (gq, gs, gv), (uq, us, uv) = mx_case(T, F, K, seed=T)
+    rh, eh = h_bounds(*product_bounds(av, gv, uv, K), "gelu")
+    h, _ = ops.mxfp8_gated_ffn(aq, as_, gq, gs, uq, us, T, F, K, act="gelu")
+    assert ((h.double() - rh).abs() <= half_step(BF, rh.abs() + eh) + eh).all()
+    q, s = ops.mxfp8_gated_ffn(aq, as_, gq, gs, uq, us, T, F, K, act="gelu", out="e4m3")
+    check_mxfp8(rh, eh, q, mma_rows(s, T, F // 32))
+    assert ops.device_status() == ops.MXN_OK
+
+
+def test_mxfp8_repeats_bit_for_bit():
+    T, F, K = 600, 1056, 512
+    (aq, as_, _), (gq, gs, _), (uq, us, _) = mx_case(T, F, K)
+    first = None
+    for _ in range(24):
+        out = ops.mxfp8_gated_ffn(aq, as_, gq, gs, uq, us, T, F, K, out="e4m3", scale_layout=ops.SCALES_ROWMAJOR)
+        first = first or out
+        assert all(torch.equal(a, b) for a, b in zip(out, first))

@@ -303,3 +303,39 @@ def test_binding_refusals():
         ops.layernorm_bwd(wide, wide, None, one, one)
     with pytest.raises(ops.MXNormError):
         ops.layernorm_fwd(torch.zeros(1, 32769, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """Rows behind the 2^31st element, forward and backward, odd and aligned row lengths."""
+    for T, D in ((66000, 32767), (140001, 16384)):
+        x = torch.empty(T, D, device="cuda", dtype=torch.bfloat16).normal_()
+        y, mean, rstd = ops.layernorm_fwd(x)
+        at = 2 ** 31 // D - 1
+        for r in (slice(0, 2), slice(at, at + 4), slice(T - 2, T)):
+            check_fwd(x[r], None, None, 1e-5, y[r], mean[r], rstd[r])
+        if D <= 16384:
+            dx, _, _ = ops.layernorm_bwd(x, y, None, mean, rstd, want_dbeta=False)
+            for r in (slice(at, at + 4), slice(T - 2, T)):
+                check_bwd(x[r], y[r], None, mean[r], rstd[r], dx[r], None, None)
+        del x, y
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own outputs and workspace, do not disturb one another."""
+    sets = []
+    for seed in (1, 2):
+        x, gamma, beta, g = make(2000, 1024, torch.bfloat16, seed=seed)
+        dy = torch.randn(2000, 1024, generator=g, device="cuda").bfloat16()
+        sets.append((x, gamma, beta, dy))
+
+    def step(x, gamma, beta, dy, stream=None):
+        y, mean, rstd = ops.layernorm_fwd(x, gamma, beta, stream=stream)
+        return (y, *ops.layernorm_bwd(x, dy, gamma, mean, rstd, stream=stream))
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        got = [step(*s, stream=st) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
