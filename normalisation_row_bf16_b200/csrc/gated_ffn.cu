@@ -245,10 +245,9 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 // stream from L2: with 256 x 256 tiles and two accumulators in turn the tensor
 // cores were busy 68% of 1456 us forward (8192 x 4096 x 14336, gate and up
 // kept), 512 x 256 moves a quarter fewer operand bytes per product and runs
-// 1291 us forward (1221 without keeping them) and 1237 and 1257 us for the two
-// products of the backward, 93% busy; copies left out, the same MMAs take 1205.
-// Back to back, under the power limit: 1449 (1358) and 3000 with the backward's
-// element-wise pass.
+// 1257 us forward and 1237 and 1257 us for the two products of the backward, 93%
+// busy; copies left out, the same MMAs take 1205.  Back to back, under the power
+// limit: 1410 to 1450 us, and 3000 to 3120 with the backward's element-wise pass.
 // Both accumulators fill at once, so a tile's epilogue is exposed, but for
 // this: the next tile's first ring of stages goes to the first accumulator
 // while the second still drains, and accumulators go back before the stores.

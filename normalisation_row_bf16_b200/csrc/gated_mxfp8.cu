@@ -5,7 +5,10 @@
 // tcgen05 scale layout: what mxnorm_fwd and mxnorm_fold_weight write).  h is
 // written as bf16, or quantised to MXFP8 in the epilogue -- E4M3 codes and E8M0
 // scales, the operand of the next product -- so the fp32 result is rounded
-// once either way and never makes a trip through memory in between.
+// once either way and never makes a trip through memory in between.  The tensor
+// cores' sums are off by about 1e-6 of an entry at K = 4096, so a value that close
+// to a rounding border takes the neighbouring code: against sums in 64 bits, 136
+// codes and no scale of 1024 x 4096 x 14336's 14.7 million and 459 thousand.
 //
 // Tiles hold 128 gate and the same 128 up features (each a whole 128-row scale
 // atom) in 256 accumulator columns.  A lane of the epilogue holds one row's
@@ -121,19 +124,21 @@ __device__ __forceinline__ void store_mxfp8(const Args& A, int row, int col, con
 // share 256 x 256 tiles; each loads 128 rows of A with their scale atom, one of
 // the two weights' 128 rows (CTA 0 gate, CTA 1 up) and both weights' atoms, and
 // CTA 0 issues tcgen05.mma.cta_group::2 for both: a third fewer operand bytes
-// from L2 than 128 x 256 tiles.  At 8192 x 4096 x 14336 pairs run 807 us (923
-// back to back, under the power limit), single CTAs 851 (997).
-// What bounds it: a stage's turn from the commit that frees it to the MMA on
-// its new contents takes about 2.5 us, so the 6 stages pass at 0.45 us each
-// where the MMAs alone would take 0.38, and a tile's change of accumulator
-// costs 1.2 us more -- 256 columns and the scales leave tensor memory no room
-// for a second one.  The MMA thread's own instructions count too: descriptors
-// built per stage and two commits a stage took 882 us.  Built and measured, not
-// kept: gate and up as two N = 128 MMAs over three rotating accumulators (1073
-// us), polling waits in place of sleeping ones (895 us).
+// from L2 than 128 x 256 tiles.  At 8192 x 4096 x 14336 it runs 653 to 688 us
+// (747 to 784 back to back, under the power limit).  K = 1024, 2048 and 4096 take
+// 227, 362 and 688 us: 0.34 to 0.42 us a stage, where the MMAs alone take about
+// 0.38 under the same clocks, and about 1.9 us a tile for its first stages and the
+// change of accumulator, which 256 columns and the scales leave tensor memory no
+// second copy of.
+// The issuing threads are what this kernel was slow by: with one thread running
+// each role's loop it took 807 us (882 with descriptors built every stage and a
+// commit per CTA), because every operand of a TMA or tcgen05 instruction then
+// moved from that thread's registers to uniform ones.  Built and measured before
+// that, not kept: gate and up as two N = 128 MMAs over three rotating
+// accumulators (1073 us), polling in place of sleeping waits (895 us).
 // Single CTAs take the calls of few rows: a stage then holds only the rows of A
 // there are (in eights), so that more stages of weights are in flight (16 rows:
-// 34.4 -> 23.6 us); the MMA's 128-row window runs on into the bytes behind
+// 34.4 -> 22.7 us); the MMA's 128-row window runs on into the bytes behind
 // them, which only reach accumulator rows that are never stored.
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_constant__ Args A) {
