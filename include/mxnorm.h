@@ -290,8 +290,9 @@ enum mxn_dtype { MXN_BF16 = 0, MXN_FP16 = 1, MXN_FP32 = 2 };
  * The squares are summed about the row's mean, so an offset far above the
  * deviation costs no accuracy.  A row with a NaN or an infinity gives NaN.
  * x       [T, ld_x] (first D columns used); any D from 1 to MXN_MAX_D, any
- *         ld_x >= D.  Rows that start on 16-byte boundaries (D and ld_x
- *         multiples of 16 bytes) move 16 bytes an access, others one element.
+ *         ld_x >= D.  Rows that all start on 16-byte boundaries (D and ld_x
+ *         multiples of 16 bytes) are the fastest: others are read through the
+ *         16-byte windows around them and written element by element.
  * gamma, beta  [D] or NULL (1 and 0).
  * y       [T, D] dense (written); must not overlap x.
  * mean, rstd   fp32 [T] (written) or NULL; the backward takes them.
@@ -353,7 +354,8 @@ int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, 
  * dh, gate, up bf16 [T, F] dense; x, w_gate, w_up, D, F, ld as in gated_ffn_fwd.
  * dx      bf16 [T, D] (written) or NULL
  * dw_gate, dw_up  bf16 [F, D] (written), or both NULL.  T = 0 writes zeros.
- * Sums are fp32, in a fixed order: no atomics.
+ * Sums are fp32, in a fixed order: no atomics.  Outputs and workspace must
+ * not overlap inputs or one another (x is read again after dx is written).
  * workspace  device scratch of at least gated_ffn_bwd_workspace_size(T, D, F)
  *         bytes, 16-byte aligned.  Contents on entry are ignored.
  */
@@ -384,7 +386,8 @@ enum mxn_ffn_out {
  * h_s     uint8, mxnorm_scales_bytes(T, F, scale_layout) bytes (written; in
  *         the MMA layout padding bytes are not), for MXN_FFN_MXFP8; else NULL
  * K a multiple of 128 (MXN_ERR_UNSUPPORTED otherwise); F a multiple of 8, of
- * 32 for MXN_FFN_MXFP8; any T (one token included).
+ * 32 for MXN_FFN_MXFP8; any T (one token included).  Outputs must not overlap
+ * inputs.
  */
 int mxfp8_gated_ffn(const void* a_q, const void* a_s, const void* g_q, const void* g_s, const void* u_q,
                     const void* u_s, void* h, void* h_s, int64_t T, int64_t F, int64_t K, int act, int out,

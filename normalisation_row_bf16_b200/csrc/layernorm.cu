@@ -137,11 +137,12 @@ struct RowPart {
   template <bool ALL>
   __device__ __forceinline__ float load_sum(uint32_t row, int c0, int n) {
     float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    // Past the row's end the last chunk is read and counts as zero: no branch a chunk.
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      u[j] = ALL || c0 + 32 * j < n ? lds128(row + 16u * (c0 + 32 * j)) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < J; ++j) u[j] = lds128(row + 16u * (ALL ? c0 + 32 * j : min(c0 + 32 * j, n - 1)));
 #pragma unroll
     for (int j = 0; j < J; ++j) {
+      if (!ALL && c0 + 32 * j >= n) u[j] = make_uint4(0, 0, 0, 0);
       float2 f[V / 2];
       unpack2<T>(u[j], f);
 #pragma unroll
@@ -151,19 +152,19 @@ struct RowPart {
   }
   template <bool ALL>
   __device__ __forceinline__ float squares(float mean, int c0, int n) const {
-    const float2 m2 = make_float2(-mean, -mean);
     float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (ALL || c0 + 32 * j < n) {
-        float2 f[V / 2];
-        unpack2<T>(u[j], f);
+    for (int j = 0; j < J; ++j) {
+      const float m = ALL || c0 + 32 * j < n ? -mean : 0.0f;
+      const float2 m2 = make_float2(m, m);
+      float2 f[V / 2];
+      unpack2<T>(u[j], f);
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-          f[e] = add2(f[e], m2);
-          acc[e & 1] = fma2(f[e], f[e], acc[e & 1]);
-        }
+      for (int e = 0; e < V / 2; ++e) {
+        f[e] = add2(f[e], m2);
+        acc[e & 1] = fma2(f[e], f[e], acc[e & 1]);
       }
+    }
     return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
   }
   // (x - mean) * rstd * gamma + beta to y (this lane's first chunk).
@@ -172,14 +173,14 @@ struct RowPart {
     const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      if (!ALL && c0 + 32 * j >= n) continue;
+      const int c = ALL ? c0 + 32 * j : min(c0 + 32 * j, n - 1);
       float2 f[V / 2], g[V / 2], b[V / 2];
       unpack2<T>(u[j], f);
-      unpack2<T>(lds128(gamma + 16u * (c0 + 32 * j)), g);
-      unpack2<T>(lds128(beta + 16u * (c0 + 32 * j)), b);
+      unpack2<T>(lds128(gamma + 16u * c), g);
+      unpack2<T>(lds128(beta + 16u * c), b);
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) f[e] = fma2(mul2(add2(f[e], m2), r2), g[e], b[e]);
-      stg128_stream(y + (size_t)32 * j * V, pack2<T>(f));
+      if (ALL || c0 + 32 * j < n) stg128_stream(y + (size_t)32 * j * V, pack2<T>(f));
     }
   }
 };
@@ -424,11 +425,14 @@ __device__ __forceinline__ void stage_params(uint8_t* dst, const T* src, int D, 
   for (int c = D / V * V + threadIdx.x; c < D; c += blockDim.x) d[c] = src[c];
 }
 
-// Threads of the ring kernel, for the registers a lane's chunks take.  Rows of
-// 16 chunks a lane measured best at 8 warps (8192 x 8192 bf16: 45.5 us, 49.6
-// with 12), shorter ones at 14 (8192 x 2048: 14.1, 14.9 with 16), single
-// elements at 20 (8000 x 5003 bf16: 48.7, 53.6 with 16).
-__host__ __device__ constexpr int ln_fwd_threads(int v, int j) { return v == 1 ? 640 : (j == 16 ? 256 : 448); }
+// Threads of the ring kernel.  Registers are dealt by the warps of an SM's
+// quarter: 255 a thread for up to 8 warps, which 14 and 16 chunks a lane need
+// (8192 x 8192 bf16: 45.5 us, 49.6 with 12 warps), 168 for up to 12; shorter rows
+// ran best at 14 warps (8192 x 2048: 14.1, 14.9 with 16), single elements at 20
+// (8000 x 5003 bf16: 48.7, 53.6 with 16).
+__host__ __device__ constexpr int ln_fwd_threads(int v, int j) {
+  return v == 1 ? 640 : (j >= 14 ? 256 : j >= 10 ? 384 : 448);
+}
 
 template <typename T, int V, int J, bool FULL>
 __global__ void __launch_bounds__(ln_fwd_threads(V, J), 1) ln_fwd_ring_kernel(const LnFwdRing R) {
@@ -850,28 +854,41 @@ int round32(int v) { return (v + 31) / 32 * 32; }
 // Columns of a partial row: D up to a 16-byte multiple.
 int part_ld(int D) { return (D + 3) / 4 * 4; }
 
+// The direct kernel of rows that plan_fwd_ring leaves or fwd() keeps from it: up
+// to 32 elements a thread, a warp a row while that covers it.  16-bit packed
+// rows come here with at most 32 chunks, single elements with at most 256 or
+// rows too long for a ring.
 template <typename T>
 const void* fwd_kernel(bool vec, int chunks, int* tpr) {
   constexpr int V = 16 / sizeof(T);
-  // Up to 32 elements a thread; a warp a row while that covers it.
-  auto pick = [&](int j) { *tpr = round32((chunks + j - 1) / j); return *tpr <= 1024; };
+  auto threads = [&](int j) { return round32((chunks + j - 1) / j); };
+  *tpr = 32;
   if (vec) {
-    if (chunks <= 32) { *tpr = 32; return (const void*)ln_fwd_kernel<T, V, 1, 1024>; }
-    if (chunks <= 64) { *tpr = 32; return (const void*)ln_fwd_kernel<T, V, 2, 1024>; }
-    if (pick(4)) return (const void*)ln_fwd_kernel<T, V, 4, 1024>;
-    pick(8);
-    if constexpr (sizeof(T) == 4) return (const void*)ln_fwd_kernel<T, V, 8, 1024>;
-    else return nullptr;
+    if constexpr (sizeof(T) == 4) {
+      if (chunks > 64) {
+        const int j = threads(4) <= 1024 ? 4 : 8;
+        *tpr = threads(j);
+        return j == 4 ? (const void*)ln_fwd_kernel<T, V, 4, 1024> : (const void*)ln_fwd_kernel<T, V, 8, 1024>;
+      }
+      if (chunks > 32) return (const void*)ln_fwd_kernel<T, V, 2, 1024>;
+    }
+    return (const void*)ln_fwd_kernel<T, V, 1, 1024>;
   }
-  if (chunks <= 256) { *tpr = 32; return (const void*)ln_fwd_kernel<T, 1, 8, 256>; }
-  pick(32);
-  if (*tpr <= 256) return (const void*)ln_fwd_kernel<T, 1, 32, 256>;
+  if (chunks <= 256) return (const void*)ln_fwd_kernel<T, 1, 8, 256>;
+  *tpr = threads(32);
   return (const void*)ln_fwd_kernel<T, 1, 32, 1024>;
 }
 
-template <typename T, int J>
-const void* fwd_ring_of(bool full) {
-  constexpr int V = 16 / sizeof(T);
+// Chunks a lane of the ring kernel holds, at most: a warp then covers 4096
+// 16-bit or 1024 fp32 elements.
+template <typename T> constexpr int kLnFwdMost = sizeof(T) == 4 ? 8 : 16;
+
+// The ring kernel of j chunks a lane, j = 1, 2 or a greater even number.
+template <typename T, int J = 1>
+const void* fwd_ring_of(int j, bool full) {
+  constexpr int V = 16 / sizeof(T), next = J == 1 ? 2 : J + 2;
+  if constexpr (next <= kLnFwdMost<T>)
+    if (j > J) return fwd_ring_of<T, next>(j, full);
   return full ? (const void*)ln_fwd_ring_kernel<T, V, J, true> : (const void*)ln_fwd_ring_kernel<T, V, J, false>;
 }
 
@@ -879,33 +896,50 @@ template <typename T>
 bool plan_fwd_ring(LnFwdRing& R, bool vec, int sms, const void** kernel, int* threads, int* grid, size_t* smem) {
   constexpr int V = 16 / sizeof(T);
   const int chunks = vec ? R.A.D / V : R.A.D;
-  int j;
-  if (vec) {
-    const int jmax = sizeof(T) == 4 ? 8 : 16;
-    for (j = 1; j < jmax && chunks > 32 * j;) j *= 2;
-    const bool full = chunks % (32 * j) == 0;
-    *kernel = j == 1 ? fwd_ring_of<T, 1>(full) : j == 2 ? fwd_ring_of<T, 2>(full) : j == 4 ? fwd_ring_of<T, 4>(full)
-            : j == 8 ? fwd_ring_of<T, 8>(full) : fwd_ring_of<T, sizeof(T) == 4 ? 8 : 16>(full);
-  } else {
-    j = chunks <= 256 ? 8 : 32;
-    *kernel = j == 8 ? (const void*)ln_fwd_ring_kernel<T, 1, 8, false> : (const void*)ln_fwd_ring_kernel<T, 1, 32, false>;
-  }
-  R.A.tpr = (chunks + j * 32 - 1) / (j * 32) * 32;
-  int ng = ln_fwd_threads(vec ? V : 1, j) / R.A.tpr;
-  if (ng < 1) return false;
-  if (R.A.tpr > 32 && ng > 15) ng = 15;            // named barriers 1..15
-  const int64_t want = (R.A.T + sms - 1) / sms;    // few rows: spread them over the SMs
-  if (want < ng) ng = (int)want;
   const size_t cap = 227 * 1024, row_bytes = sizeof(T) * (size_t)R.A.D;
   R.slot_bytes = (uint32_t)(vec ? row_bytes : (row_bytes + 15) / 16 * 16 + 16);
   R.par_bytes = (uint32_t)((row_bytes + 15) / 16 * 16);
-  auto total = [&](int stages) {
-    return 2 * (size_t)R.par_bytes + 144 + (size_t)ng * (stages * (R.slot_bytes + sizeof(uint64_t)) + 64 * sizeof(float));
+  auto total = [&](int groups, int stages) {
+    return 2 * (size_t)R.par_bytes + 144 + (size_t)groups * (stages * (R.slot_bytes + sizeof(uint64_t)) + 64 * sizeof(float));
   };
-  while (ng > 1 && total(1) > cap) --ng;
+  const int64_t want = (R.A.T + sms - 1) / sms;    // few rows: spread them over the SMs
+  auto warps_of = [&](int j) { return (chunks + j * 32 - 1) / (j * 32); };
+  auto groups_of = [&](int j) {
+    int n = ln_fwd_threads(vec ? V : 1, j) / (32 * warps_of(j));
+    if (warps_of(j) > 1 && n > 15) n = 15;         // named barriers 1..15
+    if (want < n) n = (int)want;
+    // a deep ring before a fifth group (8192 x 4096 bf16: 26.3 us with 9 groups of 2 stages, 24.0 with 8 of 3)
+    while (n > 1 && total(n, n > 4 ? 3 : 1) > cap) --n;
+    return n;
+  };
+  // Chunks a lane, by the rounds of rows and the time of one, fitted to what was
+  // measured: the SM takes 25 ns for each 32 chunks or empty places for them (21
+  // with the registers of 14 and 16 a lane, which a ragged end slows down by
+  // 0.9 us), a row alone 0.9 us and 0.055 for each of a lane's chunks; 0.2 us
+  // more for the barriers of several warps.  8192 x 5120 bf16 runs 31.1 us with
+  // 10 chunks a lane and ran 57.8 with 16, 8192 x 12288 67 with 16 and 75 with 12.
+  int j = chunks <= 256 ? 8 : 32, ng = 0;
+  if (vec) {
+    double best = 0.0;
+    for (int k = 1; k <= kLnFwdMost<T>; k += k == 1 ? 1 : 2) {
+      const int n = groups_of(k);
+      if (n < 1) continue;
+      const int warps = warps_of(k);
+      const double busy = (k >= 14 ? 0.0215 : 0.0245) * n * warps * k + 0.2, alone = 0.9 + 0.055 * k;
+      const double t = (double)((want + n - 1) / n) * ((busy > alone ? busy : alone) + (warps > 1 ? 0.2 : 0.0) +
+                                                       (k >= 14 && chunks % (32 * k) ? 0.9 : 0.0));
+      if (ng == 0 || t < best) { best = t; j = k; ng = n; }
+    }
+  } else {
+    ng = groups_of(j);
+  }
+  if (ng < 1) return false;
+  *kernel = vec ? fwd_ring_of<T>(j, chunks % (32 * j) == 0)
+                : j == 8 ? (const void*)ln_fwd_ring_kernel<T, 1, 8, false> : (const void*)ln_fwd_ring_kernel<T, 1, 32, false>;
+  R.A.tpr = 32 * warps_of(j);
   int stages = 4;
-  while (stages > 1 && total(stages) > cap) --stages;
-  if (total(stages) > cap) return false;
+  while (stages > 1 && total(ng, stages) > cap) --stages;
+  if (total(ng, stages) > cap) return false;
   R.ng = ng;
   R.stages = stages;
   R.par_off = (uint32_t)((size_t)ng * stages * R.slot_bytes);

@@ -339,3 +339,14 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+# Row lengths that take every number of chunks a lane and of warps a row, whole and ragged, few rows and many.
+@pytest.mark.parametrize("T", [3, 700])
+@pytest.mark.parametrize("D", [264, 520, 1288, 2304, 2560, 2824, 3584, 3592, 4104, 5120, 6144, 6752, 7168, 10240, 12000, 12288,
+                               14336, 20480, 24584, 32760])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_forward_plans(T, D, dtype):
+    x, gamma, beta, _ = make(T, D, dtype, seed=T + D)
+    y, mean, rstd = ops.layernorm_fwd(x, gamma, beta)
+    check_fwd(x, gamma, beta, 1e-5, y, mean, rstd)
