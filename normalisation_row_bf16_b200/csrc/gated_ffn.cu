@@ -41,10 +41,11 @@ constexpr int kGroupM = 8;                       // tiles go m-first inside grou
 struct Args {
   CUtensorMap a[2], b[2], c[3];                  // c: outputs, of pairs
   uint16_t* out[3];      // kGate: h, gate, up (the last two may be null); kDx: dx; kDw: dWg, dWu
-  float* partial;        // kDx with more than one problem: fp32 [problems, M, N] in place of dx
+  float* partial;        // with splits > 1: fp32 [problems, M, N] in place of the outputs
   unsigned* status;
   int64_t ld_out;
-  int problems;
+  int problems;          // products of one shape: 1 (kDw 2: dWg and dWu) for each split
+  int splits;            // parts that the contraction is dealt to; kDw's problem 2 s + i is part s of dW i
   int M, N;              // output rows and columns of one problem
   int m_tiles, n_tiles;  // tiles of one problem (pairs: whole 512-row tiles)
   int tiles, whole;      // work units of all problems; pairs: those that are whole 512-row tiles
@@ -176,15 +177,14 @@ __device__ __forceinline__ TilePos tile_pos(const Args& A, int t) {
   return q;
 }
 
-// k-blocks [k_lo, k_hi) of problem p.  kDx deals its contraction to `problems`
-// partial products of the same output.
+// k-blocks [k_lo, k_hi) of problem p.
 template <int MODE>
 __device__ __forceinline__ int k_lo(const Args& A, int p) {
-  return MODE == kDx ? (int)((int64_t)p * A.n_k / A.problems) : 0;
+  return MODE == kGate ? 0 : (int)((int64_t)(MODE == kDw ? p >> 1 : p) * A.n_k / A.splits);
 }
 template <int MODE>
 __device__ __forceinline__ int k_hi(const Args& A, int p) {
-  return MODE == kDx ? (int)((int64_t)(p + 1) * A.n_k / A.problems) : A.n_k;
+  return MODE == kGate ? A.n_k : (int)((int64_t)((MODE == kDw ? p >> 1 : p) + 1) * A.n_k / A.splits);
 }
 
 // 16 fp32 columns of one row of a partial product, those below n (a multiple of 8).
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
                 if constexpr (MODE == kDx) {
                   load(sa + h * kABytes, &A.a[seg], k0, m);
                 } else {
-                  load(sa + h * kABytes, &A.a[q.p], m, k0);
-                  load(sa + h * kABytes + kABytes / 2, &A.a[q.p], m + 64, k0);
+                  load(sa + h * kABytes, &A.a[q.p & 1], m, k0);
+                  load(sa + h * kABytes + kABytes / 2, &A.a[q.p & 1], m + 64, k0);
                 }
               }
               for (int c = 0; c < nb; c += 64) load(sb + c * 128, &A.b[seg], n0 + c, k0);
@@ -498,17 +498,17 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
             }
           } else {
             tmem_ld16_fence(r, true);
-            if (MODE == kDx && A.partial) {
+            if (A.partial) {
               if (live) store_cols16_f32(A.partial + ((int64_t)q.p * A.M + row) * A.N, col, end, r);
             } else {
               pack16(r, o);
-              if (live) store_cols16(A.out[MODE == kDw ? q.p : 0] + (int64_t)row * A.ld_out, col, end, o);
+              if (live) store_cols16(A.out[MODE == kDw ? q.p & 1 : 0] + (int64_t)row * A.ld_out, col, end, o);
             }
           }
           __syncwarp();                          // tcgen05.ld needs the warp converged
         }
         hand_back(acc);
-      } else if (MODE == kDx && A.partial) {
+      } else if (MODE != kGate && A.partial) {
         for (int a = 0; a < q.halves; ++a) {
           if (!wait_full((uint32_t)a)) break;
           const int row = row0 + a * 256 + lane;
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && row < A.M && col < A.N) {
-            tma_store_2d(&A.c[MODE == kGate ? b : (MODE == kDw ? q.p : 0)], box, col, row);
+            tma_store_2d(&A.c[MODE == kGate ? b : (MODE == kDw ? q.p & 1 : 0)], box, col, row);
             bulk_commit();
           }
         };
@@ -628,8 +628,10 @@ __global__ void __launch_bounds__(256) gated_act_bwd_kernel(const uint16_t* dh, 
   }
 }
 
-// dx = bf16 of the sum of the partial products [parts, n] in order: 8 elements a thread.
-__global__ void __launch_bounds__(256) gated_sum_kernel(const float* partial, int parts, int64_t n, uint16_t* dx) {
+// bf16 of the sum of the partial products [parts, n] in order, 8 elements a
+// thread; those from n0 on go to out1.
+__global__ void __launch_bounds__(256) gated_sum_kernel(const float* partial, int parts, int64_t n, int64_t n0, uint16_t* out0,
+                                                        uint16_t* out1) {
   griddep_wait();
   griddep_launch_dependents();
   for (int64_t i = 8 * ((int64_t)blockIdx.x * blockDim.x + threadIdx.x); i < n; i += 8 * (int64_t)gridDim.x * blockDim.x) {
@@ -641,7 +643,8 @@ __global__ void __launch_bounds__(256) gated_sum_kernel(const float* partial, in
       a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
       b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
     }
-    *reinterpret_cast<uint4*>(dx + i) = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+    *reinterpret_cast<uint4*>(i < n0 ? out0 + i : out1 + (i - n0)) =
+        make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
   }
 }
 
@@ -708,16 +711,18 @@ const void* kernel_of(int mode, bool pair) {
 //
 // The shape with the least estimated time, from figures measured on B200: a
 // single CTA's k-block takes as long as its bytes at 110 GB/s an SM (140 over
-// one or two rounds of tiles, 60 where they come from HBM), 0.12 us at least; a
+// one or two rounds of tiles, 60 where they come from HBM, 90 in kDw), 0.12 us at least; a
 // pair's 0.40 us for a 256-row half and 0.66 for a whole tile; a tile 1 us more
 // on single CTAs, whose epilogue overlaps (3 where the contraction is the short
 // one, over the rows), and 4.5 on pairs, 6.5 with the activation; and all
 // operands come from HBM once.  So pairs win
 // where there are several rounds of tiles (4096 x 2048 x 5632 forward 130 us,
-// 146 on single CTAs; 1000 x 1024 x 2816 19.1 and 15.9).  kDx may deal the
-// contraction to up to 8 partial products, which another kernel adds up (3 us
-// and their bytes at 6 TB/s): without it 333 x 1032 x 2744 took 25 us on 51 of
-// 148 SMs.
+// 146 on single CTAs; 1000 x 1024 x 2816 19.1 and 15.9).  The
+// backward's products may deal the contraction to up to 8 partial products,
+// which another kernel adds up (3 us and their bytes at 6 TB/s): without it the
+// dx of 333 x 1032 x 2744 took 25 us on 51 of 148 SMs, and the backward of 8192 x
+// 512 x 1408 92 us (73 with its dW split, but on single CTAs alone: 768 x 2048
+// split on pairs took 138 us, 121 whole).
 bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   constexpr uint32_t kPairStage = 3 * kABytes;
   constexpr int kPairStages = (int)((kSmemCap - kEpiWarps * kBoxBytes) / kPairStage);
@@ -736,15 +741,15 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
     best = us;
     return true;
   };
-  for (int split = 1; split <= (mode == kDx ? 8 : 1) && (split == 1 || A.n_k / split >= 4); ++split) {
+  for (int split = 1; split <= (mode == kGate ? 1 : 8) && (split == 1 || A.n_k / split >= 4); ++split) {
     const int probs = problems * split;
     const double nk = (double)A.n_k / split;
-    const double sum = split > 1 ? 3.0 + 8.0 * split * A.M * A.N / 6e6 : 0.0;
+    const double sum = split > 1 ? 3.0 + 8.0 * probs * A.M * A.N / 6e6 : 0.0;
     for (int w = widest; w >= unit; w -= unit) {
       const int64_t tiles = (int64_t)cdiv(A.M, 128) * cdiv(A.N, w) * probs, rounds = (tiles + sms - 1) / sms;
       // the second operand streams from HBM where only one row of tiles reads it
       const bool cold = A.M <= 128;
-      const double rate = rounds <= 2 ? 140e3 : 110e3;
+      const double rate = mode == kDw ? 90e3 : rounds <= 2 ? 140e3 : 110e3;
       double kb = (A.a_rows / rate + (mode == kGate ? 2 * w : w) / (cold ? 60e3 : rate)) * 128;
       if (kb < 0.12) kb = 0.12;
       const double stream = rounds * nk * kb;
@@ -752,9 +757,10 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
         L->pair = false;
         A.tile_n = w;
         A.problems = probs;
+        A.splits = split;
       }
     }
-    if (pairs > 0) {
+    if (pairs > 0 && (split == 1 || mode == kDx)) {
       const int64_t n_tiles = (int64_t)cdiv(A.N, widest) * probs, halves = cdiv(A.M, 256);
       const int64_t whole = halves / 2 * n_tiles, odd = (halves & 1) * n_tiles, rest = whole % pairs;
       const double end = mode == kGate ? 6.5 : 4.5, t1 = nk * 0.40 + end, t2 = nk * 0.66 + end;
@@ -765,6 +771,7 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
         L->pair = true;
         A.tile_n = widest;
         A.problems = probs;
+        A.splits = split;
       }
     }
   }
@@ -809,7 +816,7 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   return true;
 }
 
-// The plan of dx [T, D] = [dg du] [Wg; Wu].
+// The plans of dx [T, D] = [dg du] [Wg; Wu] and of the two dW [F, D] over T.
 bool plan_dx(Args& A, int T, int D, int F, int sms, Launch* L) {
   A.M = T;
   A.N = D;
@@ -818,12 +825,29 @@ bool plan_dx(Args& A, int T, int D, int F, int sms, Launch* L) {
   return plan_tiles(A, kDx, 1, sms, L);
 }
 
+bool plan_dw(Args& A, int T, int D, int F, int sms, Launch* L) {
+  A.M = F;
+  A.N = D;
+  A.n_k = A.n_k0 = cdiv(T, kTileK);
+  return plan_tiles(A, kDw, 2, sms, L);
+}
+
+size_t partial_bytes(const Args& A) { return A.splits > 1 ? (size_t)A.problems * A.M * A.N * sizeof(float) : 0; }
+
 // Bytes of dg and du, rounded up so that what follows stays aligned.
 size_t grads_bytes(int T, int F) { return ((size_t)4 * T * F + 255) / 256 * 256; }
 
-int launch_gemm(const Launch& L, Args& A, cudaStream_t stream, const char* what, const char** why) {
+// The product, and the sum of its parts where it was split.
+int launch_gemm(const Launch& L, Args& A, int sms, cudaStream_t stream, const char* what, const char** why) {
   void* argv[] = {&A};
-  return launch_pdl(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.pair);
+  const int e = launch_pdl(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.pair);
+  if (e || !A.partial) return e;
+  const float* partial = A.partial;
+  int64_t n0 = (int64_t)A.M * A.N, n = n0 * (A.problems / A.splits);
+  void* args[] = {&partial, &A.splits, &n, &n0, &A.out[0], &A.out[1]};
+  const int64_t need = (n / 8 + 255) / 256, cap = (int64_t)sms * 8;
+  return launch_pdl((const void*)gated_sum_kernel, (int)(need < cap ? need : cap), 256, 0, args, stream,
+                    "gated_ffn_bwd sum launch", why);
 }
 
 // Maps of the outputs (bf16 [rows, cols] dense) for store boxes.
@@ -882,14 +906,16 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
     *why = "cuTensorMapEncodeTiled failed";
     return -1;
   }
-  return launch_gemm(L, A, stream, "gated_ffn_fwd launch", why);
+  return launch_gemm(L, A, sms, stream, "gated_ffn_fwd launch", why);
 }
 
 size_t gated_ffn_bwd_workspace(int T, int D, int F, int sms) {
-  Args A{};
+  // dx is done with its parts before dW's are written
+  Args X{}, W{};
   Launch L;
-  if (!plan_dx(A, T, D, F, sms, &L)) return 0;
-  return grads_bytes(T, F) + (A.problems > 1 ? (size_t)A.problems * T * D * sizeof(float) : 0);
+  if (!plan_dx(X, T, D, F, sms, &L) || !plan_dw(W, T, D, F, sms, &L)) return 0;
+  const size_t x = partial_bytes(X), w = partial_bytes(W);
+  return grads_bytes(T, F) + (x > w ? x : w);
 }
 
 int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
@@ -908,6 +934,7 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
                                                      : (const void*)gated_act_bwd_kernel<kActGeluTanh>);
   int e = launch_pdl(k, (int)(blocks < most ? blocks : most), 256, 0, argv, stream, "gated_ffn_bwd activation launch", why);
   if (e) return e;
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grads_bytes(T, F));
   if (dx) {
     Args A{};
     Launch L;
@@ -915,25 +942,15 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     A.status = status;
     A.ld_out = D;
     if (!plan_dx(A, T, D, F, sms, &L)) { *why = "too many tiles"; return -1; }
-    if (A.problems > 1) A.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grads_bytes(T, F));
+    if (A.splits > 1) A.partial = partial;
     if (!make_map(&A.a[0], dg, T, F, F, A.a_rows) || !make_map(&A.a[1], du, T, F, F, A.a_rows) ||
         !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK) ||
         (L.pair && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";
       return -1;
     }
-    e = launch_gemm(L, A, stream, "gated_ffn_bwd dx launch", why);
+    e = launch_gemm(L, A, sms, stream, "gated_ffn_bwd dx launch", why);
     if (e) return e;
-    if (A.partial) {
-      const float* partial = A.partial;
-      int64_t n = (int64_t)T * D;
-      uint16_t* out = A.out[0];
-      void* args[] = {&partial, &A.problems, &n, &out};
-      const int64_t need = (n / 8 + 255) / 256, cap = (int64_t)sms * 8;
-      e = launch_pdl((const void*)gated_sum_kernel, (int)(need < cap ? need : cap), 256, 0, args, stream,
-                     "gated_ffn_bwd sum launch", why);
-      if (e) return e;
-    }
   }
   if (dw_gate) {
     Args A{};
@@ -941,17 +958,15 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     A.out[1] = static_cast<uint16_t*>(dw_up);
     A.status = status;
     A.ld_out = D;
-    A.M = F;
-    A.N = D;
-    A.n_k = A.n_k0 = cdiv(T, kTileK);
     Launch L;
-    if (!plan_tiles(A, kDw, 2, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (!plan_dw(A, T, D, F, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (A.splits > 1) A.partial = partial;
     if (!make_map(&A.a[0], dg, T, F, F, kTileK) || !make_map(&A.a[1], du, T, F, F, kTileK) ||
         !make_map(&A.b[0], x, T, D, ld_x, kTileK) || (L.pair && !make_out_maps(A))) {
       *why = "cuTensorMapEncodeTiled failed";
       return -1;
     }
-    e = launch_gemm(L, A, stream, "gated_ffn_bwd dw launch", why);
+    e = launch_gemm(L, A, sms, stream, "gated_ffn_bwd dw launch", why);
     if (e) return e;
   }
   return 0;

@@ -519,3 +519,20 @@ def test_mxfp8_repeats_bit_for_bit():
         out = ops.mxfp8_gated_ffn(aq, as_, gq, gs, uq, us, T, F, K, out="e4m3", scale_layout=ops.SCALES_ROWMAJOR)
         first = first or out
         assert all(torch.equal(a, b) for a, b in zip(out, first))
+
+
+# Few tiles over a long batch: the weight gradients' contraction is dealt to partial products.
+@pytest.mark.parametrize("T,D,F", [(2834, 600, 600), (4099, 136, 520), (8192, 64, 64), (3000, 1024, 1032), (4096, 512, 1408)])
+def test_backward_long_batches(T, D, F):
+    x, wg, wu = inputs(T, D, F, seed=T)
+    _, gate, up = ops.gated_ffn_fwd(x, wg, wu, save=True)
+    dh = rand((T, F), 5, 0.1)
+    first = ops.gated_ffn_bwd(dh, x, wg, wu, gate, up)
+    check_bwd(dh, x, wg, wu, gate, up, "silu", *first)
+    n = ops.gated_ffn_bwd_workspace_bytes(T, D, F)
+    ws = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    again = ops.gated_ffn_bwd(dh, x, wg, wu, gate, up, workspace=ws[:n])
+    assert all(torch.equal(a, b) for a, b in zip(first, again)) and (ws[n:] == 0xA5).all()
+    only = ops.gated_ffn_bwd(dh, x, wg, wu, gate, up, want_dx=False)
+    assert all(torch.equal(a, b) for a, b in zip(first[1:], only[1:]))
+    assert ops.device_status() == ops.MXN_OK
