@@ -7,7 +7,8 @@
 // scales, the operand of the next product -- so the fp32 result is rounded
 // once either way and never makes a trip through memory in between.  The tensor
 // cores' sums are off by about 1e-6 of an entry at K = 4096, so a value that close
-// to a rounding border takes the neighbouring code: against sums in 64 bits, 136
+// to a rounding border takes the neighbouring code (a block's maximum, the
+// neighbouring scale): against sums in 64 bits, 136
 // codes and no scale of 1024 x 4096 x 14336's 14.7 million and 459 thousand.
 //
 // Tiles hold 128 gate and the same 128 up features (each a whole 128-row scale
