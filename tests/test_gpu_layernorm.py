@@ -350,3 +350,12 @@ def test_forward_plans(T, D, dtype):
     x, gamma, beta, _ = make(T, D, dtype, seed=T + D)
     y, mean, rstd = ops.layernorm_fwd(x, gamma, beta)
     check_fwd(x, gamma, beta, 1e-5, y, mean, rstd)
+
+
+@pytest.mark.parametrize("T,D,pad", [(1, 20481, 0), (200, 30001, 0), (3, 19999, 1), (5, 32764, 1), (300, 32767, 3)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_forward_long_rows_off_boundaries(T, D, pad, dtype):
+    x, gamma, beta, _ = make(T, D, dtype, seed=T + D, pad=pad)
+    check_fwd(x, gamma, beta, 1e-5, *ops.layernorm_fwd(x, gamma, beta))
+    y, mean, rstd = ops.layernorm_fwd(x, None, None)
+    check_fwd(x, None, None, 1e-5, y, mean, rstd)
