@@ -599,6 +599,9 @@ __host__ __device__ constexpr int ln_bwd_threads(bool keep) { return keep ? 384 
 // of row sums by warps and one of columns by all threads (32 instructions an
 // element), 47.6 as here, 40.4 once the groups' column sums were folded side by
 // side instead of in turn with conflicting banks.
+// xh is the difference scaled, (x - mean) * rstd: as x * rstd - mean * rstd it takes
+// an instruction less, but then the rounding of mean * rstd shifts the whole row, by
+// 1e-5 where the mean is 1000 deviations away and 1e-3 at 100000.
 // V = 16 / sizeof(T) elements a chunk, or 1 when rows do not all start on
 // 16-byte boundaries.  gamma lies in shared memory as fp32, for V = 8 in two
 // planes of four columns a chunk, so that lanes read 16 consecutive bytes.
@@ -699,7 +702,7 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
   float m_next = n > 0 ? A.mean[g0] : 0.0f, r_next = n > 0 ? A.rstd[g0] : 0.0f;
   T* dx = static_cast<T*>(A.dx) + g0 * (int64_t)D + (size_t)c0 * V;
   for (int64_t i = 0, row = g0; i < n; ++i, row += gstep) {
-    const float a = r_next, b = -m_next * r_next;                    // xh = a x + b
+    const float a = r_next, b = -m_next;                             // xh = (x + b) a
     if (i + 1 < n) {
       m_next = A.mean[row + gstep];
       r_next = A.rstd[row + gstep];
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
         float2 xv[W], yv[W], gv[W];
         chunk_gamma(c, gv);
         if constexpr (V == 1) {
-          const float xh = fmaf(lds_elem<T>(xs + (uint32_t)sizeof(T) * c), a, b);
+          const float xh = (lds_elem<T>(xs + (uint32_t)sizeof(T) * c) + b) * a;
           const float y = lds_elem<T>(ys + (uint32_t)sizeof(T) * c), g = y * gv[0].x;
           s1.x += g;
           s2.x = fmaf(g, xh, s2.x);
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
           unpack2<T>(yu, yv);
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            const float2 xh = fma2(xv[e], a2, b2), g = mul2(yv[e], gv[e]);
+            const float2 xh = mul2(add2(xv[e], b2), a2), g = mul2(yv[e], gv[e]);
             s1 = add2(s1, g);
             s2 = fma2(g, xh, s2);
             dgam[j][e] = fma2(yv[e], xh, dgam[j][e]);
@@ -764,8 +767,8 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
     } else {
       __syncwarp();
     }
-    // dx = a (g - c1 - xh c2)
-    const float n1 = -a * (t1 * inv_d), n2 = -a * (t2 * inv_d);
+    // dx = a (g - c1 - (x + b) a c2)
+    const float n1 = -t1 * inv_d, n2 = -a * (t2 * inv_d);
     if (tid == 0 && next < A.T) {
       if (KEEP) refill(s);
       else if (A.stages > 1 && i > 0) refill(s == 0 ? A.stages - 1 : s - 1);
@@ -779,15 +782,15 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
         float2 xv[W], yv[W], gv[W];
         chunk_gamma(c, gv);
         if constexpr (V == 1) {
-          const float xh = fmaf(lds_elem<T>(xs + (uint32_t)sizeof(T) * c), a, b);
+          const float xc = lds_elem<T>(xs + (uint32_t)sizeof(T) * c) + b;
           const float y = lds_elem<T>(ys + (uint32_t)sizeof(T) * c);
-          dx[32 * j] = Elem<T>::from_f(fmaf(y * gv[0].x, a, fmaf(xh, n2, n1)));
+          dx[32 * j] = Elem<T>::from_f(fmaf(y, gv[0].x, fmaf(xc, n2, n1)) * a);
         } else {
           unpack2<T>(KEEP ? xk[KEEP ? j : 0] : lds128(xs + 16u * c), xv);
           unpack2<T>(KEEP ? yk[KEEP ? j : 0] : lds128(ys + 16u * c), yv);
 #pragma unroll
           for (int e = 0; e < W; ++e)
-            xv[e] = fma2(mul2(yv[e], gv[e]), a2, fma2(fma2(xv[e], a2, b2), n22, n12));
+            xv[e] = mul2(fma2(yv[e], gv[e], fma2(add2(xv[e], b2), n22, n12)), a2);
           stg128_stream(dx + (size_t)32 * j * V, pack2<T>(xv));
         }
       }
