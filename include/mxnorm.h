@@ -287,8 +287,10 @@ enum mxn_dtype { MXN_BF16 = 0, MXN_FP16 = 1, MXN_FP32 = 2 };
  * (above) is its form without the mean.  For every row of x, in fp32:
  *   mean = sum(x) / D,  var = sum((x - mean)^2) / D,  rstd = 1 / sqrt(var + eps)
  *   y = (x - mean) * rstd * gamma + beta               (one rounding to y's type)
- * The squares are summed about the row's mean, so an offset far above the
- * deviation costs no accuracy.  A row with a NaN or an infinity gives NaN.
+ * The squares are summed about the row's mean, and where that is far above the
+ * deviation it is corrected by the mean of what is left about it: an offset then
+ * costs no more than the rounding of mean itself, and a constant row gives beta.
+ * A row with a NaN or an infinity gives NaN.
  * x       [T, ld_x] (first D columns used); any D from 1 to MXN_MAX_D, any
  *         ld_x >= D.  Rows that all start on 16-byte boundaries (D and ld_x
  *         multiples of 16 bytes) are the fastest: others are read through the
