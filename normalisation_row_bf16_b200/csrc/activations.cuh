@@ -56,7 +56,9 @@ __device__ __forceinline__ void act_grad_f(float g, float* a, float* da) {
   } else {
     const float s = sigmoid_f(1.5957691216057308f * fmaf(0.044715f * g * g, g, g));
     *a = g * s;
-    *da = fmaf(g * s * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
+    // s (1 - s) is 0 from |g| = 16 on; the square stops there, before it overflows and makes 0 * inf of the term
+    const float b = fminf(fabsf(g), 16.0f);
+    *da = fmaf(g * s * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * b, b, 1.0f), s);
   }
 }
 
