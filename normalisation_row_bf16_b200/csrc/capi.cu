@@ -58,24 +58,31 @@ DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
 // SM count and the status word's device address for the current device,
-// looked up once per device.
+// looked up once per device.  A thread's first call on a device looks the
+// address up again, which binds the device's context to the thread: encoding a
+// tensor map is a driver call that needs one and does not bind it.
 int device_info(DeviceInfo* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   if (dev < 0 || dev >= kMaxDevices) return fail(MXN_ERR_UNSUPPORTED, "device ordinal %d", dev);
+  static thread_local uint64_t bound = 0;                            // a bit a device
+  static_assert(kMaxDevices <= 64, "one bit a device");
+  void* p = nullptr;
+  if (!(bound >> dev & 1)) {
+    e = cudaGetSymbolAddress(&p, g_mxn_status);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(status)");
+  }
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DeviceInfo& d = g_dev[dev];
   if (d.sms == 0) {
     int sms = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-    void* p = nullptr;
-    e = cudaGetSymbolAddress(&p, g_mxn_status);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(status)");
     d.status = static_cast<unsigned*>(p);
     d.sms = sms;
   }
+  bound |= 1ull << dev;
   *out = d;
   return MXN_OK;
 }
