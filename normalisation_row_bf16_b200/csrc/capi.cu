@@ -891,7 +891,7 @@ int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, 
   const char* why = "";
   const int e = gated_ffn_fwd_launch(x, w_gate, w_up, h, gate, up, (int)T, (int)D, (int)F, ld_x, ld_w, act, dev.sms,
                                      dev.status, static_cast<cudaStream_t>(stream), &why);
-  if (e) return fail(MXN_ERR_CUDA, "gated_ffn_fwd: %s", why);
+  if (e) return e > 0 ? cuda_fail((cudaError_t)e, why) : fail(MXN_ERR_CUDA, "gated_ffn_fwd: %s", why);
   return MXN_OK;
 }
 
@@ -938,7 +938,7 @@ int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void*
   const char* why = "";
   const int e = gated_ffn_bwd_launch(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace, (int)T, (int)D,
                                      (int)F, ld_x, ld_w, act, dev.sms, dev.status, s, &why);
-  if (e) return fail(MXN_ERR_CUDA, "gated_ffn_bwd: %s", why);
+  if (e) return e > 0 ? cuda_fail((cudaError_t)e, why) : fail(MXN_ERR_CUDA, "gated_ffn_bwd: %s", why);
   return MXN_OK;
 }
 
@@ -972,7 +972,7 @@ int mxfp8_gated_ffn(const void* a_q, const void* a_s, const void* g_q, const voi
   const int e = gated_mxfp8_launch(a_q, a_s, g_q, g_s, u_q, u_s, h, h_s, (int)T, (int)F, (int)K, act,
                                    scale_layout == MXN_SCALES_MMA, dev.sms, dev.status,
                                    static_cast<cudaStream_t>(stream), &why);
-  if (e) return fail(MXN_ERR_CUDA, "mxfp8_gated_ffn: %s", why);
+  if (e) return e > 0 ? cuda_fail((cudaError_t)e, why) : fail(MXN_ERR_CUDA, "mxfp8_gated_ffn: %s", why);
   return MXN_OK;
 }
 

@@ -22,6 +22,7 @@
 #include <mutex>
 
 #include "activations.cuh"
+#include "launch.h"
 #include "tcgen05.cuh"
 
 namespace mxn {
@@ -666,31 +667,6 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, in
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-int launch_pdl(const void* kernel, int grid, int threads, size_t smem, void** argv, cudaStream_t stream,
-               const char* what, const char** why, bool pair = false) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pair ? 2 : 1;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) { *why = cudaGetErrorString(e); return (int)e; }
-  }
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, argv);
-  if (e != cudaSuccess) { *why = what; return (int)e; }
-  return 0;
-}
-
 struct Launch {
   const void* kernel;
   bool pair;
@@ -840,13 +816,13 @@ size_t grads_bytes(int T, int F) { return ((size_t)4 * T * F + 255) / 256 * 256;
 // The product, and the sum of its parts where it was split.
 int launch_gemm(const Launch& L, Args& A, int sms, cudaStream_t stream, const char* what, const char** why) {
   void* argv[] = {&A};
-  const int e = launch_pdl(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.pair);
+  const int e = launch_kernel(L.kernel, L.grid, kThreads, L.smem, argv, stream, what, why, L.pair);
   if (e || !A.partial) return e;
   const float* partial = A.partial;
   int64_t n0 = (int64_t)A.M * A.N, n = n0 * (A.problems / A.splits);
   void* args[] = {&partial, &A.splits, &n, &n0, &A.out[0], &A.out[1]};
   const int64_t need = (n / 8 + 255) / 256, cap = (int64_t)sms * 8;
-  return launch_pdl((const void*)gated_sum_kernel, (int)(need < cap ? need : cap), 256, 0, args, stream,
+  return launch_kernel((const void*)gated_sum_kernel, (int)(need < cap ? need : cap), 256, 0, args, stream,
                     "gated_ffn_bwd sum launch", why);
 }
 
@@ -867,7 +843,7 @@ int cta_pair_capacity(const void* kernel, int threads, size_t smem, int slot) {
   std::lock_guard<std::mutex> lk(mu);
   if (cached[dev][slot]) return cached[dev][slot] - 1;
   int n = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
+  if (allow_shared_memory(kernel) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(threads);
@@ -932,7 +908,7 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
   const void* k = act == kActSilu ? (const void*)gated_act_bwd_kernel<kActSilu>
                                   : (act == kActGelu ? (const void*)gated_act_bwd_kernel<kActGelu>
                                                      : (const void*)gated_act_bwd_kernel<kActGeluTanh>);
-  int e = launch_pdl(k, (int)(blocks < most ? blocks : most), 256, 0, argv, stream, "gated_ffn_bwd activation launch", why);
+  int e = launch_kernel(k, (int)(blocks < most ? blocks : most), 256, 0, argv, stream, "gated_ffn_bwd activation launch", why);
   if (e) return e;
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grads_bytes(T, F));
   if (dx) {

@@ -19,6 +19,7 @@
 
 #include "activations.cuh"
 #include "gated_ffn.h"
+#include "launch.h"
 #include "tcgen05.cuh"
 
 namespace mxn {
@@ -413,27 +414,10 @@ int gated_mxfp8_launch(const void* a_q, const void* a_s, const void* g_q, const 
     *why = "cuTensorMapEncodeTiled failed";
     return -1;
   }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) { *why = cudaGetErrorString(e); return (int)e; }
   void* argv[] = {&A};
   const int units = pair ? pairs : sms;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < units ? (int)tiles : units) * (pair ? 2 : 1)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pair ? 2 : 1;
-  e = cudaLaunchKernelExC(&cfg, kernel, argv);
-  if (e != cudaSuccess) { *why = cudaGetErrorString(e); return (int)e; }
-  return 0;
+  return launch_kernel(kernel, (tiles < units ? tiles : units) * (pair ? 2 : 1), kThreads, smem, argv, stream,
+                       "mxfp8_gated_ffn launch", why, pair);
 }
 
 }  // namespace mxn

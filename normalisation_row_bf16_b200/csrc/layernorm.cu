@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "device_common.cuh"
+#include "launch.h"
 
 namespace mxn {
 namespace {
@@ -937,27 +938,6 @@ __global__ void __launch_bounds__(8 * kLnSlices) ln_dgamma_kernel(const float* p
 
 // ------------------------------------------------------------------- launches
 
-int launch(const void* kernel, int64_t grid, int threads, size_t smem, void** argv, cudaStream_t stream,
-           const char* what, const char** why) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) { *why = what; return (int)e; }
-  }
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, argv);
-  if (e != cudaSuccess) { *why = what; return (int)e; }
-  return 0;
-}
-
 int round32(int v) { return (v + 31) / 32 * 32; }
 
 // Columns of a partial row: D up to a 16-byte multiple.
@@ -1080,7 +1060,7 @@ int fwd(LnFwdArgs& A, int sms, unsigned* status, cudaStream_t stream, const char
     size_t smem;
     if (plan_fwd_ring<T>(R, vec, sms, &k, &threads, &grid, &smem)) {
       void* argv[] = {&R};
-      return launch(k, grid, threads, smem, argv, stream, "layernorm_fwd launch", why);
+      return launch_kernel(k, grid, threads, smem, argv, stream, "layernorm_fwd launch", why);
     }
   }
   const void* k = fwd_kernel<T>(vec, vec ? A.D / V : A.D, &A.tpr);
@@ -1094,7 +1074,7 @@ int fwd(LnFwdArgs& A, int sms, unsigned* status, cudaStream_t stream, const char
   int64_t grid = (A.T + rpc - 1) / rpc;
   if (grid > 0x7FFFFFFF) grid = 0x7FFFFFFF;
   void* argv[] = {&A};
-  return launch(k, grid, threads, 0, argv, stream, "layernorm_fwd launch", why);
+  return launch_kernel(k, grid, threads, 0, argv, stream, "layernorm_fwd launch", why);
 }
 
 struct LnBwdPlan {
@@ -1166,12 +1146,12 @@ int bwd(LnBwdArgs& A, void* dgamma, void* dbeta, int sms, cudaStream_t stream, c
     return (int)cudaErrorInvalidValue;
   }
   void* argv[] = {&A};
-  int e = launch(P.kernel, P.grid, P.threads, P.smem, argv, stream, "layernorm_bwd launch", why);
+  int e = launch_kernel(P.kernel, P.grid, P.threads, P.smem, argv, stream, "layernorm_bwd launch", why);
   if (e || !A.partial) return e;
   int rows = P.grid;
   const float* partial = A.partial;
   void* argr[] = {&partial, &rows, &A.D, &A.part_ld, &dgamma, &dbeta};
-  return launch((const void*)ln_dgamma_kernel<T>, (2 * A.part_ld + 31) / 32, 8 * kLnSlices, 0, argr, stream,
+  return launch_kernel((const void*)ln_dgamma_kernel<T>, (2 * A.part_ld + 31) / 32, 8 * kLnSlices, 0, argr, stream,
                 "layernorm_bwd reduction launch", why);
 }
 

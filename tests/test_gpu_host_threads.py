@@ -1,4 +1,5 @@
-"""The C entry points called from host threads of a program's own (ctypes releases the interpreter's lock)."""
+"""The C entry points called from host threads of a program's own (ctypes releases the interpreter's lock), and two sizes of
+a kernel in one graph."""
 import ctypes
 import threading
 
@@ -88,3 +89,70 @@ def test_first_cuda_call_of_a_thread(name):
     torch.cuda.synchronize()
     assert got[0][0] == ops.MXN_OK, got
     assert torch.equal(out, want)
+
+
+# Two sizes of one kernel that ask for different amounts of shared memory.
+PAIRS = {
+    "layernorm_fwd": lambda: (ln_fwd(40, 1001), ln_fwd(40, 5003)),
+    "layernorm_bwd": lambda: (ln_bwd(40, 1001), ln_bwd(40, 5003)),
+    "gated_ffn_fwd": lambda: (ffn_fwd(1, 64, 64), ffn_fwd(100, 1024, 2048)),
+    "mxfp8_gated_ffn": lambda: (mx_ffn(1, 256, 256), mx_ffn(120, 256, 256)),
+}
+
+
+@pytest.mark.parametrize("name", list(PAIRS))
+def test_two_host_threads(name):
+    """Two threads call two sizes of one kernel: each call succeeds and leaves its own result."""
+    L = ops.lib()
+    calls = PAIRS[name]()
+    want = []
+    for call, out, _ in calls:
+        assert call(L, None) == ops.MXN_OK
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    codes = [set(), set()]
+    start = threading.Barrier(2)
+
+    def work(i):
+        s = ctypes.c_void_p(streams[i].cuda_stream)
+        start.wait()
+        for _ in range(20000):
+            codes[i].add(calls[i][0](L, s))
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{ops.MXN_OK}, {ops.MXN_OK}], codes
+    for (_, out, _), w in zip(calls, want):
+        assert torch.equal(out, w)
+
+
+def test_one_graph_of_two_sizes():
+    """A graph holds both sizes of each kernel, the larger first."""
+    L = ops.lib()
+    pairs = [PAIRS[n]() for n in PAIRS]
+    want = []
+    for pair in pairs:
+        for call, out, _ in pair:
+            assert call(L, None) == ops.MXN_OK
+            torch.cuda.synchronize()
+            want.append(out.clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        for small, large in pairs:
+            assert large[0](L, s) == ops.MXN_OK and small[0](L, s) == ops.MXN_OK
+    outs = [out for pair in pairs for _, out, _ in pair]
+    for _ in range(2):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
