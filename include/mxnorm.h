@@ -358,16 +358,21 @@ int gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, void* h, 
  * dw_gate, dw_up  bf16 [F, D] (written), or both NULL.  T = 0 writes zeros.
  * Sums are fp32, in a fixed order: no atomics.  Outputs and workspace must
  * not overlap inputs or one another (x is read again after dx is written).
- * workspace  device scratch of at least gated_ffn_bwd_workspace_size(T, D, F)
- *         bytes, 16-byte aligned.  Contents on entry are ignored.
+ * workspace  device scratch, 16-byte aligned: 4 T F bytes at least (dg and du), for
+ *         the full speed gated_ffn_bwd_workspace_size(T, D, F) of this T.  Where few
+ *         tiles leave SMs idle the sums over F (dx) and over T (dW) are split, into
+ *         as many parts as there is room for; how they are split decides the order
+ *         of the sum, so results repeat bit for bit for one workspace size.
+ *         Contents on entry are ignored.
  */
 int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
                   const void* up, void* dx, void* dw_gate, void* dw_up, int64_t T, int64_t D, int64_t F, int64_t ld_x,
                   int64_t ld_w, int act, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Scratch bytes gated_ffn_bwd needs on the current device: dg and du, and
-   partial sums of dx where few rows leave SMs idle (0 if the arguments are
-   invalid). */
+/* Scratch bytes gated_ffn_bwd uses at most on the current device: dg and du, and
+   the partial sums of dx or dW where few tiles leave SMs idle (0 if the arguments
+   are invalid).  Not monotonic in T, since fewer rows may be split into more
+   parts; the workspace of a larger T serves every smaller one all the same. */
 size_t gated_ffn_bwd_workspace_size(int64_t T, int64_t D, int64_t F);
 
 /* Output of mxfp8_gated_ffn. */

@@ -274,7 +274,8 @@ PyObject* ffn_bwd(Args a) {
     r[2] = output(a[9], "dw_up", f.dev, at::kBFloat16, {f.F, f.D}, x);
   }
   size_t bytes = 0;
-  const Out ws = workspace(a[10], f.dev, (int64_t)g_lib.ffn_bwd_ws(f.T, f.D, f.F), x, &bytes);
+  const int64_t need = given(a[10]) ? 4 * f.T * f.F : (int64_t)g_lib.ffn_bwd_ws(f.T, f.D, f.F);
+  const Out ws = workspace(a[10], f.dev, need, x, &bytes);
   check(g_lib.ffn_bwd(ph, f.x, f.wg, f.wu, pg, pu, r[0].p, r[1].p, r[2].p, f.T, f.D, f.F, f.ld_x, f.ld_w,
                       (int)integer(a[6], "act"), ws.p, bytes, stream_of(a[13])));
   return tuple(r, 3);

@@ -927,17 +927,14 @@ int gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void*
   }
   if (!dx && !dw_gate) return MXN_OK;
   if (!workspace || !aligned16(workspace)) return fail(MXN_ERR_ARG, "workspace is NULL or not 16-byte aligned");
-  const size_t least = (size_t)2 * sizeof(uint16_t) * (size_t)T * (size_t)F;      // known without a device
+  const size_t least = (size_t)2 * sizeof(uint16_t) * (size_t)T * (size_t)F;      // dg and du
   if (workspace_bytes < least)
     return fail(MXN_ERR_ARG, "workspace of %zu bytes, at least %zu needed", workspace_bytes, least);
   DeviceInfo dev;
   if ((rc = device_info(&dev))) return rc;
-  const size_t need = gated_ffn_bwd_workspace((int)T, (int)D, (int)F, dev.sms);
-  if (workspace_bytes < need)
-    return fail(MXN_ERR_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   const char* why = "";
-  const int e = gated_ffn_bwd_launch(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace, (int)T, (int)D,
-                                     (int)F, ld_x, ld_w, act, dev.sms, dev.status, s, &why);
+  const int e = gated_ffn_bwd_launch(dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace, workspace_bytes,
+                                     (int)T, (int)D, (int)F, ld_x, ld_w, act, dev.sms, dev.status, s, &why);
   if (e) return e > 0 ? cuda_fail((cudaError_t)e, why) : fail(MXN_ERR_CUDA, "gated_ffn_bwd: %s", why);
   return MXN_OK;
 }

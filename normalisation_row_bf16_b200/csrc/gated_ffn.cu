@@ -674,6 +674,9 @@ struct Launch {
   size_t smem;
 };
 
+// Bytes of fp32 partial products of `problems` problems.
+size_t partial_bytes(const Args& A, int problems) { return (size_t)problems * A.M * A.N * sizeof(float); }
+
 template <int MODE>
 const void* kernel_of(bool pair) {
   return pair ? (const void*)gated_gemm_kernel<MODE, true> : (const void*)gated_gemm_kernel<MODE, false>;
@@ -682,8 +685,21 @@ const void* kernel_of(int mode, bool pair) {
   return mode == kGate ? kernel_of<kGate>(pair) : mode == kDx ? kernel_of<kDx>(pair) : kernel_of<kDw>(pair);
 }
 
-// Fills the tile and ring geometry of a launch from A's M, N and n_k.  Returns
-// false when the tiles outnumber an int.
+// Ring of a CTA pair.
+constexpr uint32_t kPairStage = 3 * kABytes;
+constexpr int kPairStages = (int)((kSmemCap - kEpiWarps * kBoxBytes) / kPairStage);
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + kEpiWarps * kBoxBytes + sizeof(Barriers);
+
+// Pairs of CTAs that the current device runs at once.
+int pairs_at_once(int mode, int sms) {
+  const int pairs = cta_pair_capacity(kernel_of(mode, true), kThreads, kPairSmem, mode);
+  return pairs > sms / 2 ? sms / 2 : pairs;
+}
+
+// Fills the tile and ring geometry of a launch from A's M, N and n_k, for `sms`
+// SMs that run `pairs` CTA pairs at once (none are taken for at most 128 rows),
+// with `room` bytes for partial products.  Returns false when the tiles
+// outnumber an int.
 //
 // The shape with the least estimated time, from figures measured on B200: a
 // single CTA's k-block takes as long as its bytes at 110 GB/s an SM (140 over
@@ -699,17 +715,10 @@ const void* kernel_of(int mode, bool pair) {
 // dx of 333 x 1032 x 2744 took 25 us on 51 of 148 SMs, and the backward of 8192 x
 // 512 x 1408 92 us (73 with its dW split, but on single CTAs alone: 768 x 2048
 // split on pairs took 138 us, 121 whole).
-bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
-  constexpr uint32_t kPairStage = 3 * kABytes;
-  constexpr int kPairStages = (int)((kSmemCap - kEpiWarps * kBoxBytes) / kPairStage);
-  constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + kEpiWarps * kBoxBytes + sizeof(Barriers);
+bool plan_tiles(Args& A, int mode, int problems, int sms, int pairs, size_t room, Launch* L) {
   const int unit = mode == kGate ? 8 : 64, widest = mode == kGate ? 128 : 256;
   A.a_rows = mode == kDw || A.M >= 128 ? 128 : (A.M + 7) / 8 * 8;
-  int pairs = 0;
-  if (A.M > 128) {
-    pairs = cta_pair_capacity(kernel_of(mode, true), kThreads, kPairSmem, mode);
-    if (pairs > sms / 2) pairs = sms / 2;
-  }
+  if (A.M <= 128) pairs = 0;
   const double hbm = 128.0 * A.n_k * (A.M + (double)A.N * (mode == kGate ? 2 : 1)) * (mode == kDw ? 2 : 1) / 6.5e6;
   double best = 0;
   auto better = [&](double us) {
@@ -719,6 +728,7 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   };
   for (int split = 1; split <= (mode == kGate ? 1 : 8) && (split == 1 || A.n_k / split >= 4); ++split) {
     const int probs = problems * split;
+    if (split > 1 && partial_bytes(A, probs) > room) break;
     const double nk = (double)A.n_k / split;
     const double sum = split > 1 ? 3.0 + 8.0 * probs * A.M * A.N / 6e6 : 0.0;
     for (int w = widest; w >= unit; w -= unit) {
@@ -792,25 +802,31 @@ bool plan_tiles(Args& A, int mode, int problems, int sms, Launch* L) {
   return true;
 }
 
-// The plans of dx [T, D] = [dg du] [Wg; Wu] and of the two dW [F, D] over T.
-bool plan_dx(Args& A, int T, int D, int F, int sms, Launch* L) {
+// The plans of gate and up [T, F] over D, of dx [T, D] = [dg du] [Wg; Wu] and of
+// the two dW [F, D] over T.
+bool plan_fwd(Args& A, int T, int D, int F, int sms, int pairs, Launch* L) {
+  A.M = T;
+  A.N = F;
+  A.n_k = A.n_k0 = cdiv(D, kTileK);
+  return plan_tiles(A, kGate, 1, sms, pairs, 0, L);
+}
+
+bool plan_dx(Args& A, int T, int D, int F, int sms, int pairs, size_t room, Launch* L) {
   A.M = T;
   A.N = D;
   A.n_k0 = cdiv(F, kTileK);
   A.n_k = 2 * A.n_k0;
-  return plan_tiles(A, kDx, 1, sms, L);
+  return plan_tiles(A, kDx, 1, sms, pairs, room, L);
 }
 
-bool plan_dw(Args& A, int T, int D, int F, int sms, Launch* L) {
+bool plan_dw(Args& A, int T, int D, int F, int sms, int pairs, size_t room, Launch* L) {
   A.M = F;
   A.N = D;
   A.n_k = A.n_k0 = cdiv(T, kTileK);
-  return plan_tiles(A, kDw, 2, sms, L);
+  return plan_tiles(A, kDw, 2, sms, pairs, room, L);
 }
 
-size_t partial_bytes(const Args& A) { return A.splits > 1 ? (size_t)A.problems * A.M * A.N * sizeof(float) : 0; }
-
-// Bytes of dg and du, rounded up so that what follows stays aligned.
+// Bytes of dg and du, rounded up so that the partial products behind them stay aligned.
 size_t grads_bytes(int T, int F) { return ((size_t)4 * T * F + 255) / 256 * 256; }
 
 // The product, and the sum of its parts where it was split.
@@ -871,12 +887,9 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
   A.out[2] = static_cast<uint16_t*>(up);
   A.status = status;
   A.ld_out = F;
-  A.M = T;
-  A.N = F;
   A.act = act;
-  A.n_k = A.n_k0 = cdiv(D, kTileK);
   Launch L;
-  if (!plan_tiles(A, kGate, 1, sms, &L)) { *why = "too many tiles"; return -1; }
+  if (!plan_fwd(A, T, D, F, sms, T > 128 ? pairs_at_once(kGate, sms) : 0, &L)) { *why = "too many tiles"; return -1; }
   if (!make_map(&A.a[0], x, T, D, ld_x, A.a_rows) || !make_map(&A.b[0], w_gate, F, D, ld_w, A.tile_n) ||
       !make_map(&A.b[1], w_up, F, D, ld_w, A.tile_n) || (L.pair && !make_out_maps(A))) {
     *why = "cuTensorMapEncodeTiled failed";
@@ -889,14 +902,16 @@ size_t gated_ffn_bwd_workspace(int T, int D, int F, int sms) {
   // dx is done with its parts before dW's are written
   Args X{}, W{};
   Launch L;
-  if (!plan_dx(X, T, D, F, sms, &L) || !plan_dw(W, T, D, F, sms, &L)) return 0;
-  const size_t x = partial_bytes(X), w = partial_bytes(W);
+  if (!plan_dx(X, T, D, F, sms, T > 128 ? pairs_at_once(kDx, sms) : 0, SIZE_MAX, &L) ||
+      !plan_dw(W, T, D, F, sms, F > 128 ? pairs_at_once(kDw, sms) : 0, SIZE_MAX, &L))
+    return 0;
+  const size_t x = X.splits > 1 ? partial_bytes(X, X.problems) : 0, w = W.splits > 1 ? partial_bytes(W, W.problems) : 0;
   return grads_bytes(T, F) + (x > w ? x : w);
 }
 
 int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
-                         const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace, int T, int D, int F,
-                         int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
+                         const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
+                         int T, int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
                          const char** why) {
   uint16_t* dg = static_cast<uint16_t*>(workspace);
   uint16_t* du = dg + (int64_t)T * F;
@@ -911,13 +926,14 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
   int e = launch_kernel(k, (int)(blocks < most ? blocks : most), 256, 0, argv, stream, "gated_ffn_bwd activation launch", why);
   if (e) return e;
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grads_bytes(T, F));
+  const size_t room = workspace_bytes > grads_bytes(T, F) ? workspace_bytes - grads_bytes(T, F) : 0;
   if (dx) {
     Args A{};
     Launch L;
     A.out[0] = static_cast<uint16_t*>(dx);
     A.status = status;
     A.ld_out = D;
-    if (!plan_dx(A, T, D, F, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (!plan_dx(A, T, D, F, sms, T > 128 ? pairs_at_once(kDx, sms) : 0, room, &L)) { *why = "too many tiles"; return -1; }
     if (A.splits > 1) A.partial = partial;
     if (!make_map(&A.a[0], dg, T, F, F, A.a_rows) || !make_map(&A.a[1], du, T, F, F, A.a_rows) ||
         !make_map(&A.b[0], w_gate, F, D, ld_w, kTileK) || !make_map(&A.b[1], w_up, F, D, ld_w, kTileK) ||
@@ -935,7 +951,7 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
     A.status = status;
     A.ld_out = D;
     Launch L;
-    if (!plan_dw(A, T, D, F, sms, &L)) { *why = "too many tiles"; return -1; }
+    if (!plan_dw(A, T, D, F, sms, F > 128 ? pairs_at_once(kDw, sms) : 0, room, &L)) { *why = "too many tiles"; return -1; }
     if (A.splits > 1) A.partial = partial;
     if (!make_map(&A.a[0], dg, T, F, F, kTileK) || !make_map(&A.a[1], du, T, F, F, kTileK) ||
         !make_map(&A.b[0], x, T, D, ld_x, kTileK) || (L.pair && !make_out_maps(A))) {

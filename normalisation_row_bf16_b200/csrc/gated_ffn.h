@@ -15,14 +15,15 @@ int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, vo
                          int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
                          cudaStream_t stream, const char** why);
 
-// Scratch of the backward: dg and du, and dx's partial products where it splits
-// the contraction.
+// Scratch of the backward: dg and du, and the partial products of dx or of dW
+// (one after the other in the same place) where few tiles split the contraction.
 size_t gated_ffn_bwd_workspace(int T, int D, int F, int sms);
 
-// dx, and the pair dw_gate, dw_up, may be null.
+// dx, and the pair dw_gate, dw_up, may be null.  workspace_bytes: at least dg and
+// du's (4 T F); contractions are split into the parts that the rest has room for.
 int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
-                         const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace, int T, int D, int F,
-                         int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status, cudaStream_t stream,
-                         const char** why);
+                         const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
+                         int T, int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
+                         cudaStream_t stream, const char** why);
 
 }  // namespace mxn

@@ -389,7 +389,9 @@ def gated_ffn_bwd_workspace_bytes(T: int, D: int, F: int) -> int:
 def gated_ffn_bwd(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None, dw_gate=None, dw_up=None,
                   workspace=None, want_dx: bool = True, want_dw: bool = True, stream=None):
     """Backward of gated_ffn_fwd from the gate and up it kept: returns
-    (dx [T, D], dw_gate [F, D], dw_up [F, D]), None where not wanted."""
+    (dx [T, D], dw_gate [F, D], dw_up [F, D]), None where not wanted.
+    workspace: 4 T F bytes at least, gated_ffn_bwd_workspace_bytes for the full
+    speed; that of a larger T serves a smaller one."""
     return _launch(_binding().gated_ffn_bwd, x, stream,
                    (dh, x, w_gate, w_up, gate, up, _choice(ACT, act, "activation"), dx, dw_gate, dw_up, workspace,
                     want_dx, want_dw))
