@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
     uint32_t it = 0, uses[2] = {0, 0};
     bool ok = true;
     auto wait_full = [&](uint32_t acc) {
-      ok = mbar_wait_bounded(&S.acc_full[acc], uses[acc]++ & 1u, A.status) && !failed_flag(S);
+      // by vote: the tcgen05.ld of the next tile needs the whole warp, whichever lane's wait gave up
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.acc_full[acc], uses[acc]++ & 1u, A.status) && !failed_flag(S));
       tc_fence_after();
       if (!ok && lane == 0) atomicOr(&S.failed, 1u);
       return ok;

@@ -283,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) gated_mxfp8_kernel(const __grid_c
     for (int t = first; t < tiles; t += step, ++it) {
       int mt, nt;
       tile_pos(A, t, &mt, &nt);
-      const bool got = mbar_wait_bounded(&S.acc_full, it & 1u, A.status);
+      // by vote: the tcgen05.ld of the next tile needs the whole warp, whichever lane's wait gave up
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.acc_full, it & 1u, A.status) && !failed_flag(S));
       tc_fence_after();
-      if (!got || failed_flag(S)) {
+      if (!got) {
         if (lane == 0) atomicOr(&S.failed, 1u);
         break;
       }

@@ -210,9 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     for (int t = blockIdx.x; t < n_tiles_all; t += gridDim.x, ++it) {
       const int mt = t % m_tiles, nt = t / m_tiles;
-      const bool got = mbar_wait_bounded(&S.acc_full, it & 1u, status);
+      // by vote: the tcgen05.ld below need the whole warp, whichever lane's wait gave up
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.acc_full, it & 1u, status) && !failed_flag(S));
       tc_fence_after();
-      if (!got || failed_flag(S)) {
+      if (!got) {
         if (lane == 0) atomicOr(&S.failed, 1u);
         break;
       }
@@ -483,9 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     for (int t = (int)cid; t < n_tiles_all; t += (int)ncl, ++it) {
       const int mt = t % m_tiles, nt = t / m_tiles;
-      const bool got = mbar_wait_bounded(&S.acc_full, it & 1u, status);
+      // by vote: the tcgen05.ld below need the whole warp, whichever lane's wait gave up
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.acc_full, it & 1u, status) && !failed_flag2(S));
       tc_fence_after();
-      if (!got || failed_flag2(S)) {
+      if (!got) {
         if (lane == 0) atomicOr(&S.failed, 1u);
         break;
       }
@@ -754,9 +756,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
     uint32_t it = 0;
     for (int t = blockIdx.x; t < n_tiles_all; t += gridDim.x, ++it) {
       const int mt = t % m_tiles, nt = t / m_tiles;
-      const bool got = mbar_wait_bounded(&S.acc_full, it & 1u, status);
+      // by vote: the tcgen05.ld below need the whole warp, whichever lane's wait gave up
+      const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&S.acc_full, it & 1u, status) && !failed_flag_w(S));
       tc_fence_after();
-      if (!got || failed_flag_w(S)) {
+      if (!got) {
         if (lane == 0) atomicOr(&S.failed, 1u);
         break;
       }
