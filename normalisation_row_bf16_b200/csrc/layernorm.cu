@@ -504,6 +504,14 @@ __device__ __forceinline__ void copy_window(uint8_t* slot, const T* src, uint32_
     bulk_copy_g2s(slot, reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15), bytes, bar, pol);
 }
 
+// After a wait gave up, leave no copy in flight: the thread that fetched `issued`
+// rows (and fetches none once its wait gave up, since that stage's barrier is still
+// armed) waits, bounded, for the last phase of every stage.
+__device__ __forceinline__ void drain(uint64_t* full, int stages, int64_t issued, unsigned* status) {
+  for (int64_t k = issued > stages ? issued - stages : 0; k < issued; ++k)
+    mbar_wait_bounded(&full[k % stages], (uint32_t)(k / stages) & 1u, status);
+}
+
 // gamma or beta to shared memory as stored (16-byte aligned at both ends), by
 // the whole CTA; a constant when there is none.
 template <typename T>
@@ -596,7 +604,7 @@ __global__ void __launch_bounds__(ln_fwd_threads(V, J), 1) ln_fwd_ring_kernel(co
     fence_proxy_async_smem();              // these reads before the refill's bulk copy
     float mean = group_sum(sum, red, nwarp, 1 + group) * inv_d;
     if (nwarp == 1) __syncwarp();
-    if (tid == 0 && left > 0) refill(s);
+    if (tid == 0 && ok && left > 0) refill(s);
     if (++s == R.stages) { s = 0; ph ^= 1u; }
     sum = all ? v.template squares<true>(mean, c0, nchunk) : v.template squares<false>(mean, c0, nchunk);
     float var = group_sum(sum, red + 128u, nwarp, 1 + group) * inv_d;
@@ -615,6 +623,7 @@ __global__ void __launch_bounds__(ln_fwd_threads(V, J), 1) ln_fwd_ring_kernel(co
     else v.template store<false>(y, mean, rstd, params, params + R.par_bytes, c0, nchunk);
     y += gstep * A.D;
   }
+  if (tid == 0 && !ok) drain(full, R.stages, n - left, R.status);
 }
 
 // ------------------------------------------------------------------- backward
@@ -822,7 +831,7 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
     }
     // dx = a (g - c1 - (x + b) a c2)
     const float n1 = -t1 * inv_d, n2 = -a * (t2 * inv_d);
-    if (tid == 0 && next < A.T) {
+    if (tid == 0 && ok && next < A.T) {
       if (KEEP) refill(s);
       else if (A.stages > 1 && i > 0) refill(s == 0 ? A.stages - 1 : s - 1);
     }
@@ -856,12 +865,14 @@ __global__ void __launch_bounds__(ln_bwd_threads(KEEP), 1) ln_bwd_kernel(const L
       if (A.stages == 1) {
         if (nwarp > 1) named_barrier_sync(1 + group, A.tpr);
         else __syncwarp();
-        if (tid == 0 && next < A.T) refill(0);
+        if (tid == 0 && ok && next < A.T) refill(0);
       }
     }
     dx += gstep * D;
     if (++s == A.stages) { s = 0; ph ^= 1u; }
   }
+
+  if (tid == 0 && !ok) drain(full, A.stages, (next - g0) / gstep, A.status);
 
   if (!A.partial) return;
   // The CTA's sums: every group lays its own out in shared memory (each copy

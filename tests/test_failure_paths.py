@@ -22,3 +22,19 @@ def test_epilogues_leave_by_vote(name, waits):
     assert len(found) == waits
     for stmt in found:
         assert re.search(r"__all_sync\(0xFFFFFFFFu, mbar_wait_bounded\(&S\.acc_full.*failed_flag", stmt, re.S), stmt
+
+
+@pytest.mark.parametrize("kernel", ["ln_fwd_ring_kernel", "ln_bwd_kernel"])
+def test_row_rings_stop_and_drain(kernel):
+    """A ring whose wait gave up is fetched into no more (its stage's barrier is still armed) and its copies in flight
+    are waited for before the block ends."""
+    s = source("layernorm.cu")
+    at = s.index("void __launch_bounds__", s.index("struct LnFwdRing")) if kernel == "ln_fwd_ring_kernel" else 0
+    body = s[s.index(kernel + "(", at):]
+    body = body[:body.index("\n}\n")]
+    loop = body[body.index("bool ok = true;"):]
+    guards = re.findall(r"if \(tid == 0([^{;]*?)\) (?:\{\s*if \(KEEP\) )?refill\(", loop)
+    assert guards and all("&& ok &&" in g for g in guards), guards
+    assert re.search(r"if \(tid == 0 && !ok\) drain\(", loop)
+    if "A.partial" in loop:
+        assert loop.index("drain(") < loop.index("if (!A.partial) return;")
