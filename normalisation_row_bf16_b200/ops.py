@@ -330,10 +330,19 @@ def _binding():
     return _binding_module
 
 
+def _use_on(stream, tensors):
+    """Tells the allocator that work on `stream` uses the tensors: memory that the
+    caller gives up is then reused only after that work."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+
+
 def _launch(fn, x, stream, args):
     """fn(*args, stream handle): on the current stream of x's device, or on
     `stream`, inside which outputs and workspaces are then allocated -- memory
-    of that stream, so that the allocator orders its reuse after the kernels."""
+    of that stream, so that the allocator orders its reuse after the kernels --
+    and on which the inputs are recorded."""
     if stream is None:
         on_gpu = isinstance(x, torch.Tensor) and x.is_cuda
         return fn(*args, torch._C._cuda_getCurrentRawStream(x.get_device()) if on_gpu else 0)
@@ -345,7 +354,10 @@ def _launch(fn, x, stream, args):
     if stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     with torch.cuda.stream(stream):
-        return fn(*args, stream.cuda_stream)
+        out = fn(*args, stream.cuda_stream)
+    if stream != torch.cuda.current_stream(dev):
+        _use_on(stream, args)
+    return out
 
 
 def layernorm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
