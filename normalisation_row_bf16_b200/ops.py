@@ -8,6 +8,7 @@ tensors, raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import importlib.util
 import math
 import os
@@ -96,6 +97,33 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _use_on(stream, tensors):
+    """Tells the allocator that work on `stream` uses the tensors: memory that the
+    caller gives up is then reused only after that work."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+
+
+def _on_stream(op):
+    """With stream= another stream than the current one, an operator runs inside
+    it: outputs and workspaces it allocates are memory of that stream, and its
+    tensor arguments are recorded on it."""
+    @functools.wraps(op)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return op(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        if stream == torch.cuda.current_stream(stream.device):
+            return op(*args, stream=stream, **kw)
+        with torch.cuda.stream(stream):
+            out = op(*args, stream=stream, **kw)
+        _use_on(stream, (*args, *kw.values()))
+        return out
+    return call
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -148,6 +176,7 @@ def _alloc_outputs(x, T, D, layout, q, scales, elem: str = "e4m3"):
     return q, scales
 
 
+@_on_stream
 def mxnorm_fwd(x, gamma=None, p: float = 2.0, rounding: int = RNE, seed: int = 0,
                scale_layout: int = SCALES_ROWMAJOR, q=None, scales=None, G=None, stream=None):
     """MXNorm forward: returns (q uint8 [T, D] E4M3 codes, scales uint8 E8M0, G fp32 [T])."""
@@ -163,6 +192,7 @@ def mxnorm_fwd(x, gamma=None, p: float = 2.0, rounding: int = RNE, seed: int = 0
     return q, scales, G
 
 
+@_on_stream
 def mxfp8_cast(x, rounding: int = RNE, seed: int = 0, scale_layout: int = SCALES_ROWMAJOR,
                q=None, scales=None, stream=None):
     """MX quantisation of x itself: (q uint8 [T, D], scales uint8)."""
@@ -173,6 +203,7 @@ def mxfp8_cast(x, rounding: int = RNE, seed: int = 0, scale_layout: int = SCALES
     return q, scales
 
 
+@_on_stream
 def mxnorm_fwd_ex(x, gamma=None, p: float = 2.0, rounding: int = RNE, seed: int = 0,
                   scale_layout: int = SCALES_ROWMAJOR, elem: str = "e4m3", stat: str = "absmax",
                   q=None, scales=None, G=None, stream=None):
@@ -190,6 +221,7 @@ def mxnorm_fwd_ex(x, gamma=None, p: float = 2.0, rounding: int = RNE, seed: int 
     return q, scales, G
 
 
+@_on_stream
 def mx_cast(x, gain=None, rounding: int = RNE, seed: int = 0, scale_layout: int = SCALES_ROWMAJOR,
             elem: str = "e4m3", q=None, scales=None, stream=None):
     """MX quantisation of x, or of x * gain along each row: (q, scales)."""
@@ -202,6 +234,7 @@ def mx_cast(x, gain=None, rounding: int = RNE, seed: int = 0, scale_layout: int 
     return q, scales
 
 
+@_on_stream
 def fold_weight(w, gamma, elem: str = "e4m3", scale_layout: int = SCALES_MMA, q=None, scales=None,
                 stream=None):
     """MXNormLinear folding: MX codes and scales of w[n, k] * gamma[k], w [N, K]
@@ -214,6 +247,7 @@ def fold_weight(w, gamma, elem: str = "e4m3", scale_layout: int = SCALES_MMA, q=
     return q, scales
 
 
+@_on_stream
 def rmsnorm_bf16(x, gamma=None, eps: float = 1e-5, y=None, stream=None):
     T, D, ld = _rows_ld(x)
     gamma = _bf16_vec(gamma, D)
@@ -224,6 +258,7 @@ def rmsnorm_bf16(x, gamma=None, eps: float = 1e-5, y=None, stream=None):
     return y
 
 
+@_on_stream
 def rmsnorm_then_mxcast(x, gamma=None, eps: float = 1e-5, scale_layout: int = SCALES_ROWMAJOR,
                         y_tmp=None, q=None, scales=None, stream=None):
     """Two-pass comparator: (q, scales, y_tmp)."""
@@ -242,6 +277,7 @@ def bwd_workspace_bytes(T: int, D: int) -> int:
     return int(lib().mxnorm_bwd_workspace_size(T, D))
 
 
+@_on_stream
 def mxnorm_bwd(x, dy, gamma, G, dx=None, dgamma=None, workspace=None, want_dgamma: bool = True,
                stream=None):
     """STE backward: returns (dx bf16 [T, D], dgamma bf16 [D] or None)."""
@@ -268,6 +304,7 @@ def mxnorm_bwd(x, dy, gamma, G, dx=None, dgamma=None, workspace=None, want_dgamm
     return dx, dgamma
 
 
+@_on_stream
 def mxnorm_bwd_noalloc(x, dy, gamma, G, dx=None, dgamma=None, want_dgamma: bool = True,
                        stream=None):
     """The backward through the entry point that allocates no device memory
@@ -289,6 +326,7 @@ def mxnorm_bwd_noalloc(x, dy, gamma, G, dx=None, dgamma=None, want_dgamma: bool 
     return dx, dgamma
 
 
+@_on_stream
 def mxfp8_gemm(a_q, a_s, b_q, b_s, M: int, N: int, K: int, c=None, stream=None):
     """C bf16 [M, N] = dequant(A) @ dequant(B)^T; scales in the MMA layout."""
     for t in (a_q, a_s, b_q, b_s):
@@ -328,14 +366,6 @@ def _binding():
         m.set_library(MXNormError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
         _binding_module = m
     return _binding_module
-
-
-def _use_on(stream, tensors):
-    """Tells the allocator that work on `stream` uses the tensors: memory that the
-    caller gives up is then reused only after that work."""
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
 
 
 def _launch(fn, x, stream, args):
@@ -444,4 +474,4 @@ def algorithmic_bytes_fwd(T: int, D: int, gamma: bool = True, G_out: bool = True
     return T * D * 2 + T * D + T * (D // 32) + (2 * D if gamma else 0) + (4 * T if G_out else 0)
 
 
-__all__ = [n for n in dir() if not n.startswith("_") and n not in ("ctypes", "importlib", "math", "os", "torch")]
+__all__ = [n for n in dir() if not n.startswith("_") and n not in ("ctypes", "functools", "importlib", "math", "os", "torch")]

@@ -102,3 +102,30 @@ def test_forked_stream_in_a_graph(name):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     del args, got, g
     torch.cuda.empty_cache()
+
+
+def _mxnorm_bwd_inputs():
+    x, dy = _ln_args()
+    gamma = torch.ones(1024, device="cuda", dtype=BF)
+    return [x, dy, gamma, ops.mxnorm_fwd(x, gamma)[2]]
+
+
+OLD = {
+    "mxnorm_fwd": (_ln_args, lambda a, **k: ops.mxnorm_fwd(a[0], **k)),
+    "mxnorm_fwd_ex": (_ln_args, lambda a, **k: ops.mxnorm_fwd_ex(a[0], elem="nvfp4", **k)),
+    "mxfp8_cast": (_ln_args, lambda a, **k: ops.mxfp8_cast(a[0], **k)),
+    "mx_cast": (_ln_args, lambda a, **k: ops.mx_cast(a[0], elem="e2m1", **k)),
+    "fold_weight": (_ln_args, lambda a, **k: ops.fold_weight(a[0], a[1][0].contiguous(), **k)),
+    "rmsnorm_bf16": (_ln_args, lambda a, **k: ops.rmsnorm_bf16(a[0], **k)),
+    "rmsnorm_then_mxcast": (_ln_args, lambda a, **k: ops.rmsnorm_then_mxcast(a[0], **k)),
+    "mxnorm_bwd": (_mxnorm_bwd_inputs, lambda a, **k: ops.mxnorm_bwd(*a, **k)),
+    "mxnorm_bwd_noalloc": (_mxnorm_bwd_inputs, lambda a, **k: ops.mxnorm_bwd_noalloc(*a, **k)),
+    "mxfp8_gemm": (_mx_args, lambda a, **k: ops.mxfp8_gemm(a[0], a[1], a[2], a[3], 256, 512, 256, **k)),
+}
+
+
+@pytest.mark.parametrize("name", list(OLD))
+def test_inputs_dropped_behind_an_older_call_on_another_stream(name):
+    want, got, taken = dropped_inputs(*OLD[name])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((t == 0x7B).all() for t in taken)
