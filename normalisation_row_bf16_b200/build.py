@@ -1,21 +1,22 @@
-"""Builds libmxnorm_b200.so in-tree with nvcc for sm_100a (no JIT cache), and the
-Python module that marshals torch tensors for it (_binding.so, host code only).
+"""Builds libmxnorm_b200.so in-tree with nvcc for sm_100a (no JIT cache), and where
+torch is installed the Python module that marshals its tensors (host code only).
 
     python -m normalisation_row_bf16_b200.build
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxnorm_b200.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xptxas", "-warn-spills"]
@@ -23,7 +24,7 @@ NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", 
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def _older(target: str, srcs) -> bool:
@@ -37,8 +38,20 @@ def is_stale() -> bool:
     return _older(LIB, sources())
 
 
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def binding_path() -> str:
+    """The binding module for this interpreter and this torch: it is compiled
+    against the headers of both, so another version's is not loaded."""
+    import torch
+
+    return os.path.join(PKG, f"_binding.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def binding_is_stale() -> bool:
-    return _older(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return _older(binding_path(), [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def nvcc() -> str:
@@ -50,12 +63,10 @@ def nvcc() -> str:
 
 def _start_binding(verbose: bool):
     """Starts the compiler on the binding module: (process, temporary output)."""
-    import sysconfig
-
     import torch
     from torch.utils import cpp_extension
 
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = binding_path() + f".tmp{os.getpid()}"
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     inc += cpp_extension.include_paths()
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -69,15 +80,30 @@ def _start_binding(verbose: bool):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every translation unit in csrc/ (in parallel) and link the
-    library, and the binding module beside it."""
-    binding = _start_binding(verbose) if force or binding_is_stale() else None
+    library, and the binding module beside it.  The library does not depend on
+    torch: without it, or where the binding does not compile, it is built all the
+    same (and the failure raised after it)."""
+    binding = why = None
+    if not has_torch():
+        if verbose:
+            print("no torch: building the library without its Python binding", file=sys.stderr)
+    else:
+        try:
+            if force or binding_is_stale():
+                binding = _start_binding(verbose)
+        except Exception as e:  # noqa: BLE001 -- a broken torch or no C++ compiler
+            why = e
     try:
-        return _build_library(force, verbose)
+        lib = _build_library(force, verbose)
     finally:
         if binding:
-            if binding[0].wait() != 0:
-                raise RuntimeError("the binding module did not compile")
-            os.replace(binding[1], BINDING)
+            if binding[0].wait() == 0:
+                os.replace(binding[1], binding_path())
+            else:
+                why = RuntimeError("the compiler failed")
+    if why is not None:
+        raise RuntimeError("the binding module was not built") from why
+    return lib
 
 
 def _build_library(force: bool, verbose: bool) -> str:

@@ -355,10 +355,11 @@ def _binding():
     global _binding_module
     if _binding_module is None:
         L = lib()
-        if not os.path.exists(_build.BINDING):
-            raise RuntimeError(f"{_build.BINDING} is missing: run `python -m normalisation_row_bf16_b200.build` "
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: run `python -m normalisation_row_bf16_b200.build` "
                                "(there is no CPU fallback)")
-        spec = importlib.util.spec_from_file_location("normalisation_row_bf16_b200._binding", _build.BINDING)
+        spec = importlib.util.spec_from_file_location("normalisation_row_bf16_b200._binding", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         names = ("layernorm_fwd", "layernorm_bwd", "layernorm_bwd_workspace_size", "gated_ffn_fwd", "gated_ffn_bwd",
