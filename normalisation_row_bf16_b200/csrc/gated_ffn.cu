@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_gemm_kernel(const __grid_co
           __syncwarp();                          // tcgen05.ld needs the warp converged
         }
         hand_back(acc);
-      } else if (MODE != kGate && A.partial) {
+      } else if (MODE == kDx && A.partial) {     // of the products on pairs only dx is ever split
         for (int a = 0; a < q.halves; ++a) {
           if (!wait_full((uint32_t)a)) break;
           const int row = row0 + a * 256 + lane;

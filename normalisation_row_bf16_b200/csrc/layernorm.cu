@@ -1018,7 +1018,7 @@ bool plan_fwd_ring(LnFwdRing& R, bool vec, int sms, const void** kernel, int* th
   // 0.9 us), a row alone 0.9 us and 0.055 for each of a lane's chunks; 0.2 us
   // more for the barriers of several warps.  8192 x 5120 bf16 runs 31.1 us with
   // 10 chunks a lane and ran 57.8 with 16, 8192 x 12288 67 with 16 and 75 with 12.
-  int j = chunks <= 256 ? 8 : 32, ng = 0;
+  int j = 32, ng = 0;                              // single elements: rows of more than 256
   if (vec) {
     double best = 0.0;
     for (int k = 1; k <= kLnFwdMost<T>; k += k == 1 ? 1 : 2) {
@@ -1034,8 +1034,7 @@ bool plan_fwd_ring(LnFwdRing& R, bool vec, int sms, const void** kernel, int* th
     ng = groups_of(j);
   }
   if (ng < 1) return false;
-  *kernel = vec ? fwd_ring_of<T>(j, chunks % (32 * j) == 0)
-                : j == 8 ? (const void*)ln_fwd_ring_kernel<T, 1, 8, false> : (const void*)ln_fwd_ring_kernel<T, 1, 32, false>;
+  *kernel = vec ? fwd_ring_of<T>(j, chunks % (32 * j) == 0) : (const void*)ln_fwd_ring_kernel<T, 1, 32, false>;
   R.A.tpr = 32 * warps_of(j);
   int stages = 4;
   while (stages > 1 && total(ng, stages) > cap) --stages;
