@@ -453,6 +453,26 @@ void mxnorm_debug_fail_next(int count);
  */
 int mxnorm_debug_wait_timeout(uint64_t limit_ns, int* gave_up, void* stream);
 
+/* Product of a feed-forward operator. */
+enum mxn_ffn_product {
+    MXN_PLAN_FWD = 0,   /* gate and up of gated_ffn_fwd */
+    MXN_PLAN_DX = 1,    /* dx of gated_ffn_bwd */
+    MXN_PLAN_DW = 2,    /* dw_gate and dw_up of gated_ffn_bwd */
+    MXN_PLAN_MXFP8 = 3  /* mxfp8_gated_ffn, with K for D */
+};
+
+/*
+ * Debug query, on the host alone: how a product of T rows is dealt to a device
+ * of `sms` SMs that runs `pairs` pairs of CTAs at once (sms = 0: the current
+ * device's figures).  workspace_bytes as passed to gated_ffn_bwd, for its two
+ * products.  plan (host memory, 8 ints): whether CTA pairs take it, output
+ * columns of a tile, parts of the contraction, work units, of them whole 512-row
+ * tiles, halves of tiles past the last full round and odd 256-row halves (pairs
+ * of the bf16 products), and CTAs launched.
+ */
+int mxnorm_debug_ffn_plan(int product, int64_t T, int64_t D, int64_t F, int sms, int pairs, size_t workspace_bytes,
+                          int* plan);
+
 #ifdef __cplusplus
 }
 #endif

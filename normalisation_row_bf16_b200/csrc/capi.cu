@@ -973,6 +973,40 @@ int mxfp8_gated_ffn(const void* a_q, const void* a_s, const void* g_q, const voi
   return MXN_OK;
 }
 
+int mxnorm_debug_ffn_plan(int product, int64_t T, int64_t D, int64_t F, int sms, int pairs, size_t workspace_bytes,
+                          int* plan) {
+  t_err.clear();
+  const bool mx = product == MXN_PLAN_MXFP8;
+  int rc = mx ? MXN_OK : check_ffn(T, D, F, D, D, MXN_ACT_SILU);
+  if (!rc && (product < MXN_PLAN_FWD || product > MXN_PLAN_MXFP8)) rc = fail(MXN_ERR_ARG, "product = %d", product);
+  if (!rc && (T <= 0 || T > kFfnMax || D <= 0 || F <= 0 || F > kFfnMax || !plan || sms < 0 || pairs < 0))
+    rc = fail(MXN_ERR_ARG, "bad arguments");
+  if (rc) return rc;
+  if (sms == 0) {
+    DeviceInfo dev;
+    if ((rc = device_info(&dev))) return rc;
+    sms = dev.sms;
+    pairs = mx ? gated_mxfp8_pairs_at_once(sms) : gated_ffn_pairs(product, sms);
+  }
+  FfnPlan P{};
+  if (mx) {
+    int64_t units;
+    P.pair = gated_mxfp8_pairs((int)T, (int)F, sms, pairs, &units);
+    const int at_once = P.pair ? pairs : sms;
+    P.tile_n = 128;
+    P.splits = 1;
+    P.units = (int)(units < 0x7FFFFFFF ? units : 0x7FFFFFFF);
+    P.grid = (P.units < at_once ? P.units : at_once) * (P.pair ? 2 : 1);
+  } else {
+    const size_t grads = ((size_t)4 * T * F + 255) / 256 * 256;
+    if (!gated_ffn_plan(product, (int)T, (int)D, (int)F, sms, pairs, workspace_bytes > grads ? workspace_bytes - grads : 0, &P))
+      return fail(MXN_ERR_UNSUPPORTED, "too many tiles");
+  }
+  const int out[8] = {P.pair, P.tile_n, P.splits, P.units, P.whole, P.dealt, P.odd, P.grid};
+  for (int i = 0; i < 8; ++i) plan[i] = out[i];
+  return MXN_OK;
+}
+
 int mxnorm_debug_wait_timeout(uint64_t limit_ns, int* gave_up, void* stream) {
   t_err.clear();
   t_empty = false;

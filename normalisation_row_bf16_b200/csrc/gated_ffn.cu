@@ -879,6 +879,21 @@ int cta_pair_capacity(const void* kernel, int threads, size_t smem, int slot) {
   return n;
 }
 
+bool gated_ffn_plan(int product, int T, int D, int F, int sms, int pairs, size_t room, FfnPlan* plan) {
+  Args A{};
+  Launch L;
+  const bool ok = product == kPlanGate ? plan_fwd(A, T, D, F, sms, pairs, &L)
+                  : product == kPlanDx ? plan_dx(A, T, D, F, sms, pairs, room, &L)
+                                       : plan_dw(A, T, D, F, sms, pairs, room, &L);
+  if (!ok) return false;
+  const int odd = L.pair ? odd_halves(A) : 0;
+  *plan = FfnPlan{L.pair, A.tile_n, A.splits, A.tiles, L.pair ? A.whole : 0, L.pair ? A.tiles - A.whole - odd : 0, odd,
+                  L.grid};
+  return true;
+}
+
+int gated_ffn_pairs(int product, int sms) { return pairs_at_once(product, sms); }
+
 int gated_ffn_fwd_launch(const void* x, const void* w_gate, const void* w_up, void* h, void* gate, void* up, int T,
                          int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
                          cudaStream_t stream, const char** why) {

@@ -26,4 +26,16 @@ int gated_ffn_bwd_launch(const void* dh, const void* x, const void* w_gate, cons
                          int T, int D, int F, int64_t ld_x, int64_t ld_w, int act, int sms, unsigned* status,
                          cudaStream_t stream, const char** why);
 
+// How a product is dealt to `sms` SMs that run `pairs` CTA pairs at once, with `room` bytes for partial products: host
+// arithmetic alone.
+struct FfnPlan {
+  int pair, tile_n, splits;          // CTA pairs; output columns of a tile; parts of the contraction
+  int units, whole, dealt, odd;      // work units; of them, for pairs: 512-row tiles, halves of tiles that were dealt out, odd halves
+  int grid;                          // CTAs
+};
+enum { kPlanGate = 0, kPlanDx = 1, kPlanDw = 2 };
+bool gated_ffn_plan(int product, int T, int D, int F, int sms, int pairs, size_t room, FfnPlan* plan);
+// The pairs that the current device runs at once.
+int gated_ffn_pairs(int product, int sms);
+
 }  // namespace mxn

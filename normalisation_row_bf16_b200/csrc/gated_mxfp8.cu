@@ -355,7 +355,29 @@ bool make_sf_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K) {
   return make_map(map, base, (rows + 127) / 128 * (K / kTileK) * 4, 128, 4, false);
 }
 
+// Ring of a CTA pair.
+constexpr size_t kCap = 227 * 1024 - 512;
+static_assert(sizeof(Barriers) <= 512, "barrier block");
+constexpr uint32_t kPairStage = 2 * kRows128 + 2048;               // 1024-aligned
+constexpr int kPairStages = (int)(kCap / kPairStage) < kMaxStages ? (int)(kCap / kPairStage) : kMaxStages;
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + sizeof(Barriers);
+
 }  // namespace
+
+int gated_mxfp8_pairs_at_once(int sms) {
+  const int pairs = cta_pair_capacity((const void*)gated_mxfp8_kernel<true>, kThreads, kPairSmem, 3);
+  return pairs > sms / 2 ? sms / 2 : pairs;
+}
+
+// Pairs where their 256-row tiles take fewer rounds of tile time (twice the
+// work of a 128-row tile on two SMs).
+bool gated_mxfp8_pairs(int T, int F, int sms, int pairs, int64_t* units) {
+  const int64_t n_tiles = (F + kTileF - 1) / kTileF;
+  const int64_t t1 = (int64_t)((T + 127) / 128) * n_tiles, t2 = (int64_t)((T + 255) / 256) * n_tiles;
+  const bool pair = T > 128 && pairs > 0 && (t2 + pairs - 1) / pairs <= (t1 + sms - 1) / sms;
+  *units = pair ? t2 : t1;
+  return pair;
+}
 
 int gated_mxfp8_launch(const void* a_q, const void* a_s, const void* g_q, const void* g_s, const void* u_q,
                        const void* u_s, void* h, void* h_s, int T, int F, int K, int act, bool scale_mma, int sms,
@@ -373,23 +395,11 @@ int gated_mxfp8_launch(const void* a_q, const void* a_s, const void* g_q, const 
   A.act = act;
   A.out = !h_s ? 0 : (scale_mma ? 2 : 1);
   A.n_tiles = (F + kTileF - 1) / kTileF;
-  constexpr size_t kCap = 227 * 1024 - 512;
-  static_assert(sizeof(Barriers) <= 512, "barrier block");
 
-  // Pairs where their 256-row tiles take fewer rounds of tile time (twice the
-  // work of a 128-row tile on two SMs).
   const void* kernel = (const void*)gated_mxfp8_kernel<true>;
-  constexpr uint32_t kPairStage = 2 * kRows128 + 2048;             // 1024-aligned
-  constexpr int kPairStages = (int)(kCap / kPairStage) < kMaxStages ? (int)(kCap / kPairStage) : kMaxStages;
-  constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + sizeof(Barriers);
-  int pairs = 0;
-  if (T > 128) {
-    pairs = cta_pair_capacity(kernel, kThreads, kPairSmem, 3);
-    if (pairs > sms / 2) pairs = sms / 2;
-  }
-  const int64_t t1 = (int64_t)((T + 127) / 128) * A.n_tiles, t2 = (int64_t)((T + 255) / 256) * A.n_tiles;
-  const bool pair = pairs > 0 && (t2 + pairs - 1) / pairs <= (t1 + sms - 1) / sms;
-  const int64_t tiles = pair ? t2 : t1;
+  const int pairs = T > 128 ? gated_mxfp8_pairs_at_once(sms) : 0;
+  int64_t tiles;
+  const bool pair = gated_mxfp8_pairs(T, F, sms, pairs, &tiles);
   if (tiles > 0x7FFFFFFF - sms) {
     *why = "too many tiles";
     return -1;

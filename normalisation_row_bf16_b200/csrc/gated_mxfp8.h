@@ -14,4 +14,9 @@ int gated_mxfp8_launch(const void* a_q, const void* a_s, const void* g_q, const 
                        const void* u_s, void* h, void* h_s, int T, int F, int K, int act, bool scale_mma, int sms,
                        unsigned* status, cudaStream_t stream, const char** why);
 
+// Whether the call takes CTA pairs, on `sms` SMs that run `pairs` of them at once, and its work units.
+bool gated_mxfp8_pairs(int T, int F, int sms, int pairs, int64_t* units);
+// The pairs that the current device runs at once.
+int gated_mxfp8_pairs_at_once(int sms);
+
 }  // namespace mxn

@@ -51,6 +51,7 @@ SIGNATURES = {
     "gated_ffn_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P, _SZ, _P]),
     "gated_ffn_bwd_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "mxfp8_gated_ffn": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P]),
+    "mxnorm_debug_ffn_plan": (_I32, [_I32, _I64, _I64, _I64, _I32, _I32, _SZ, _P]),
     "mxnorm_last_error": (ctypes.c_char_p, []),
     "mxnorm_device_status": (_I32, [_P]),
     "mxnorm_set_tuning": (_I32, [_I32, _I32, _I32]),
