@@ -294,17 +294,44 @@ __device__ __forceinline__ void each_element(const T* x, int D, int tid, int thr
   }
 }
 
+// The same for rows on 16-byte boundaries, without the columns: four chunks of V
+// elements ahead.
+template <typename T, int V, typename F>
+__device__ __forceinline__ void each_of(const T* x, int D, int tid, int threads, F f) {
+  if constexpr (V == 1) {
+    each_element(x, D, tid, threads, [&](int, float v) { f(v); });
+  } else {
+    const int n = D / V;
+#pragma unroll 1
+    for (int c = tid; c < n; c += 4 * threads) {
+      uint4 u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = ldg128_nc(x + (int64_t)min(c + k * threads, n - 1) * V);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k * threads < n) {
+          float v[V];
+          unpack16<T, V>(u[k], v);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f(v[e]);
+        }
+    }
+  }
+}
+
 // The second mean and the variance about it, from the row in memory, so that the
-// common path keeps no register for them: 8000 x 5003 bf16, no row of it far, runs
-// 50.7 us (48.3 without this, 54.3 from the registers' copy of the row), 8192 x 4096
-// bf16 24.0 (23.8).  sum(v, i): the row's sum of v, the i-th asked for.
-template <typename T, typename S>
+// common path keeps no register for them.  With no row far 8000 x 5003 bf16 runs
+// 49.9 us (48.3 without any of this, 54.3 with it from the registers' copy of the
+// row, 51.8 not out of line) and 8192 x 4096 bf16 24.0 (23.9); with every row far
+// 8192 x 4096 takes 57 us in bf16 and 104 in fp32.  sum(v, i): the row's sum of v,
+// the i-th asked for.
+template <typename T, int V, typename S>
 __device__ __forceinline__ void refine(const T* x, int D, int tid, int threads, float inv_d, S sum, float* mean, float* var) {
   float m = *mean, s = 0.0f;
-  each_element(x, D, tid, threads, [&](int, float v) { s += v - m; });
+  each_of<T, V>(x, D, tid, threads, [&](float v) { s += v - m; });
   m += sum(s, 0) * inv_d;
   s = 0.0f;
-  each_element(x, D, tid, threads, [&](int, float v) { s = fmaf(v - m, v - m, s); });
+  each_of<T, V>(x, D, tid, threads, [&](float v) { s = fmaf(v - m, v - m, s); });
   *var = sum(s, 1) * inv_d;
   *mean = m;
 }
@@ -371,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) ln_fwd_kernel(const LnFwdArgs A) {
     float var = row_sum(q, 1) * inv_d;
     if (far_mean<T>(mean, var)) {
       const float first = mean;
-      refine(x, A.D, tid, A.tpr, inv_d, row_sum, &mean, &var);
+      refine<T, V>(x, A.D, tid, A.tpr, inv_d, row_sum, &mean, &var);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -442,7 +469,7 @@ __global__ void __launch_bounds__(kLnLongThreads, 1) ln_fwd_long_kernel(const Ln
     float mean = row_sum(s, 0) * inv_d;
     each([&](int, float v) { q = fmaf(v - mean, v - mean, q); });
     float var = row_sum(q, 1) * inv_d;
-    if (far_mean<T>(mean, var)) refine(x, D, tid, kLnLongThreads, inv_d, row_sum, &mean, &var);
+    if (far_mean<T>(mean, var)) refine<T, 1>(x, D, tid, kLnLongThreads, inv_d, row_sum, &mean, &var);
     const float rstd = rsqrtf(var + A.eps);
     if (tid == 0) {
       if (A.mean) A.mean[row] = mean;
@@ -542,6 +569,15 @@ __host__ __device__ constexpr int ln_fwd_threads(int v, int j) {
   return v == 1 ? 640 : (j >= 14 ? 256 : j >= 10 ? 384 : 448);
 }
 
+// refine() over a row group of the ring kernel, out of line.
+template <typename T, int V>
+__device__ __noinline__ float2 refine_group(const T* x, int D, int tid, int threads, float mean, uint32_t red, int barrier) {
+  float var;
+  refine<T, V>(x, D, tid, threads, 1.0f / (float)D,
+               [&](float v, int i) { return group_sum(v, red + 128u * i, threads >> 5, barrier); }, &mean, &var);
+  return make_float2(mean, var);
+}
+
 template <typename T, int V, int J, bool FULL>
 __global__ void __launch_bounds__(ln_fwd_threads(V, J), 1) ln_fwd_ring_kernel(const LnFwdRing R) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -610,8 +646,9 @@ __global__ void __launch_bounds__(ln_fwd_threads(V, J), 1) ln_fwd_ring_kernel(co
     float var = group_sum(sum, red + 128u, nwarp, 1 + group) * inv_d;
     if (far_mean<T>(mean, var)) {
       const float first = mean;
-      refine(x0 + row * A.ld_x, A.D, tid, A.tpr, inv_d,
-             [&](float v, int i) { return group_sum(v, red + 128u * i, nwarp, 1 + group); }, &mean, &var);
+      const float2 mv = refine_group<T, V>(x0 + row * A.ld_x, A.D, tid, A.tpr, mean, red, 1 + group);
+      mean = mv.x;
+      var = mv.y;
       v.shift(mean - first);
     }
     const float rstd = rsqrtf(var + A.eps);
