@@ -7,7 +7,8 @@
 //   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x
 // Products accumulate in fp32 tensor memory; h, dx and the weight gradients are
 // rounded once to bf16.  dg and du are rounded to bf16 because they are
-// tensor-core operands (one rounding of 2^-9 each, as large as an output's).
+// tensor-core operands (one rounding of at most 2^-8 each, as large as an output's;
+// the relative error of dx, dWg and dWu goes from 0.0017 to 0.0023 by it).
 //
 // One kernel does the three products (Mode):
 //   kGate  one tile holds the gate and the up columns of the same features, so

@@ -9,8 +9,8 @@
 // Arithmetic and every sum are fp32; y, dx, dgamma and dbeta are rounded once.
 // Both passes are bound by HBM: 2 (forward) and 3 (backward) elements move per
 // element of x, with about 8 and 14 flops each.  At 8192 x 4096 bf16 the forward
-// runs 24.0 us (5.6 TB/s, 0.87 of a measured copy) and the backward 40.4 us with
-// the reduction of dgamma and dbeta (5.0 TB/s, 0.77); fp32 45.9 and 68.8 us (0.90
+// runs 24.1 us (5.6 TB/s, 0.86 of a measured copy) and the backward 40.2 us with
+// the reduction of dgamma and dbeta (5.0 TB/s, 0.78); fp32 46.1 and 68.6 us (0.90
 // and 0.91).  16-bit elements cost twice the instructions a byte, so the work is
 // in packed fp32 pairs on rows held in registers, few reductions, and copies
 // that need no thread.
